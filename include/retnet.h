@@ -427,6 +427,120 @@ RETNET_API retnet_status_t retnet_debug_set_wait_budget(long long cycles);
  */
 RETNET_API retnet_status_t retnet_fp16_range_errors(unsigned int* count, int clear);
 
+/*
+ * ---- Serving: sequences packed in one token axis, their states in a pool ----------------------
+ *
+ * A pool is a caller-owned device array fp32 [slots][heads_kv][d_k][d_v]: one slot holds the state
+ * of one sequence, all heads.  heads_kv key/value heads are each shared by heads / heads_kv query
+ * heads (query head i reads key/value head i / (heads / heads_kv)); gamma is per key/value head.
+ *
+ * Rows of q, k, v, o are tokens; the heads of a row are contiguous, rows are stride_* elements
+ * apart (a row of a fused projection's output may be passed as it is).
+ *
+ * slots, pos and cu_seqlens are DEVICE arrays, read by the kernels: a captured graph may be
+ * replayed with other contents.  What they hold cannot be checked on the host; a sequence that they
+ * name wrongly (a slot >= slots, a slot that an earlier sequence of the call with tokens has, a
+ * negative position) is left out: its rows of o and the pool stay as they were, and
+ * retnet_slot_errors counts it.  A sequence with slot < 0 is padding: left out and not counted.
+ */
+typedef struct {
+    int64_t tokens;   /* rows of q, k, v, o */
+    int64_t seqs;     /* sequences: entries of slots and pos; at most 65535 */
+    int64_t heads, heads_kv;
+    int64_t d_k, d_v;
+    int64_t slots;    /* slots of the pool */
+    int64_t stride_q, stride_k, stride_v, stride_o; /* elements between rows */
+} retnet_packed_t;
+
+/*
+ * Retention (§2.4, its chunkwise form) over packed sequences.  Sequence i owns the rows
+ * cu_seqlens[i] .. cu_seqlens[i+1]-1 (int32, seqs + 1 entries, not decreasing, the last at most
+ * tokens; a call whose cu_seqlens is not so does nothing and counts one error).  Its first token is
+ * at absolute position pos[i] (int64; pos NULL: all 0).  At position 0 it starts from a zero state,
+ * whatever its slot holds; at a later one it continues from pool[slots[i]].  The state after its
+ * last token goes to pool[slots[i]].  A sequence without tokens leaves its slot as it was.  Rows of
+ * o that belong to no sequence stay as they were.
+ *   dtype: of q, k, v and o.  gamma: host float[heads_kv]; theta: host float[d_k/2].
+ *   flags: XPOS, SCALE_SQRT_D, NORM_D; RETNET_F_NORM_R is RETNET_ERR_UNSUPPORTED;
+ *   RETNET_F_PRECISE keeps the call on the fp32 CUDA-core kernels.
+ *   workspace: device, 16-byte aligned, at least retnet_packed_workspace_size bytes, in use until
+ *   the call's work completes; two calls that share one must be ordered on the device.
+ *   o and pool overlap no other argument.
+ * The pool is updated in fp32.  A token whose q, k or v is not finite may make the outputs of up to
+ * 255 earlier tokens of its own sequence not finite; it reaches no other sequence.
+ */
+RETNET_API retnet_status_t retnet_retention_packed(const void* q, const void* k, const void* v, void* o,
+                                        retnet_packed_t dims, retnet_dtype_t dtype, const float* gamma,
+                                        const float* theta, uint32_t flags, const int32_t* cu_seqlens,
+                                        const int32_t* slots, const int64_t* pos, float* pool,
+                                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of retnet_retention_packed (strides, heads and slots are not read). */
+RETNET_API retnet_status_t retnet_packed_workspace_size(retnet_packed_t dims, size_t* bytes);
+
+/*
+ * Its single-token form (§2.2): row i is one token, at absolute position pos[i], of the sequence in
+ * slot slots[i]; S <- gamma S + k^T v in place (from zeros at position 0), then o = q S with the
+ * flags' factors.  tokens == seqs.  Each named state is read once and written once.  Rows left out
+ * (above; every row counts as a sequence with tokens) keep their o.  Other arguments as
+ * retnet_retention_packed; no workspace.
+ */
+RETNET_API retnet_status_t retnet_retention_step_slots(const void* q, const void* k, const void* v, void* o,
+                                            retnet_packed_t dims, retnet_dtype_t dtype,
+                                            const float* gamma, const float* theta, uint32_t flags,
+                                            const int32_t* slots, const int64_t* pos, float* pool,
+                                            void* stream);
+
+/*
+ * pool[dst[i]] <- pool[src[i]] for all pairs at once, every source read as it was before the call:
+ * forking (one source, many destinations), compacting (live slots into holes), reordering in place
+ * (a permutation, a beam's parents), freeing (src < 0: zeros).  pool: fp32 [slots][slot_floats],
+ * 16-byte aligned.  src, dst: device int32[pairs], pairs <= RETNET_MAX_SLOT_PAIRS.  dst < 0 is
+ * padding.  A pair with a slot >= slots, or with the destination of an earlier pair, is left out and
+ * counted by retnet_slot_errors.
+ */
+#define RETNET_MAX_SLOT_PAIRS 1024
+RETNET_API retnet_status_t retnet_state_slots_copy(float* pool, int64_t slots, int64_t slot_floats,
+                                        const int32_t* src, const int32_t* dst, int64_t pairs,
+                                        void* stream);
+
+/*
+ * Count of sequences, rows and pairs that the three calls above left out since the last clear.
+ * Synchronises with the device; with clear != 0 the count is reset.  RETNET_OK or RETNET_ERR_CUDA.
+ */
+RETNET_API retnet_status_t retnet_slot_errors(unsigned int* count, int clear);
+
+/*
+ * ---- MSR epilogue with a learnable affine (§三.2), and its gradient ----------------------------
+ *
+ * out = swish(g) (.) (weight (.) GroupNorm_h(y) + bias): the normalisation of retnet_msr_epilogue
+ * (groups are the d_v values of a (token, head) row, biased variance, eps >= 0 inside the root).
+ *   y, g, out: [tokens][heads][d_v] dtype, dense; d_v from 1 to RETNET_MAX_DV, no multiple of
+ *   anything (rows of a multiple of 8 values in 16-byte aligned buffers go fastest).
+ *   weight, bias: device fp32 [heads][d_v], NULL: ones, zeros.  out may alias y or g.
+ */
+RETNET_API retnet_status_t retnet_msr_affine(const void* y, const void* g, const float* weight, const float* bias,
+                                  void* out, int64_t tokens, int64_t heads, int64_t d_v, float eps,
+                                  retnet_dtype_t dtype, void* stream);
+
+/*
+ * Gradient of retnet_msr_affine (with weight = bias = NULL, of retnet_msr_epilogue): for dout =
+ * dL/dout, dy and dg in dtype, and the sums over tokens dweight, dbias in fp32 [heads][d_v] (each
+ * may be NULL: not computed).  The sums are added in a fixed order: the same bits every time.
+ *   dy and dg overlap no input.
+ *   workspace: device, 16-byte aligned, retnet_msr_affine_workspace_size bytes; not needed (NULL)
+ *   without dweight and dbias.  Without tokens, dweight and dbias are cleared.
+ */
+RETNET_API retnet_status_t retnet_msr_affine_backward(const void* y, const void* g, const float* weight,
+                                           const float* bias, const void* dout, void* dy, void* dg,
+                                           float* dweight, float* dbias, int64_t tokens, int64_t heads,
+                                           int64_t d_v, float eps, retnet_dtype_t dtype,
+                                           void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of retnet_msr_affine_backward. */
+RETNET_API retnet_status_t retnet_msr_affine_workspace_size(int64_t tokens, int64_t heads, int64_t d_v,
+                                                 size_t* bytes);
+
 /* Static, NUL-terminated description of a status code (never NULL). */
 RETNET_API const char* retnet_status_string(retnet_status_t status);
 

@@ -12,6 +12,10 @@ The functions carry the C names:
   retnet_msr_epilogue         -- §三.2 GroupNorm per head, then the swish gate
   retnet_msr_chunkwise        -- §2.4 and §三.2 in one kernel (the retention output stays on chip)
   retnet_retention_backward   -- gradient of the forward (dq, dk, dv, d state) for training
+  retnet_retention_packed     -- §2.4 for ragged sequences packed in one token axis, states in a pool
+  retnet_retention_step_slots -- §2.2 for rows that each name a pool slot and a position
+  retnet_state_slots_copy     -- forking, compacting, reordering and freeing pool slots
+  retnet_msr_affine, retnet_msr_affine_backward -- §三.2 with a learnable affine, and its gradient
 with the §三.3 normalisations chosen by flags.  Tensors are dense BLHD (see the header).
 """
 import ctypes
@@ -41,7 +45,10 @@ EXPORTS = ("retnet_retention_parallel", "retnet_retention_chunkwise", "retnet_re
            "retnet_backward_workspace_size", "retnet_backward_kernel", "retnet_backward_launches",
            "retnet_chunkwise_kernel", "retnet_chunkwise_launches", "retnet_debug_wait_timeouts",
            "retnet_fp16_range_errors", "retnet_debug_set_wait_budget",
-           "retnet_status_string", "retnet_version")
+           "retnet_retention_packed", "retnet_packed_workspace_size", "retnet_retention_step_slots",
+           "retnet_state_slots_copy", "retnet_slot_errors", "retnet_msr_affine", "retnet_msr_affine_backward",
+           "retnet_msr_affine_workspace_size", "retnet_status_string", "retnet_version")
+MAX_SLOT_PAIRS = 1024  # RETNET_MAX_SLOT_PAIRS
 
 
 class RetnetError(RuntimeError):
@@ -53,6 +60,11 @@ class RetnetError(RuntimeError):
 class Dims(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("heads", ctypes.c_int64),
                 ("d_k", ctypes.c_int64), ("d_v", ctypes.c_int64)]
+
+
+class PackedDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("tokens", "seqs", "heads", "heads_kv", "d_k", "d_v", "slots", "stride_q",
+                                              "stride_k", "stride_v", "stride_o")]
 
 
 _lib = None
@@ -116,6 +128,22 @@ def load(path: str = None):
     lib.retnet_fp16_range_errors.restype = _i32
     lib.retnet_debug_set_wait_budget.argtypes = [ctypes.c_longlong]
     lib.retnet_debug_set_wait_budget.restype = _i32
+    _sz = ctypes.c_size_t
+    lib.retnet_retention_packed.argtypes = [_vp, _vp, _vp, _vp, PackedDims, _i32, _fp, _fp, _u32, _vp, _vp, _vp, _vp,
+                                            _vp, _sz, _vp]
+    lib.retnet_packed_workspace_size.argtypes = [PackedDims, ctypes.POINTER(_sz)]
+    lib.retnet_retention_step_slots.argtypes = [_vp, _vp, _vp, _vp, PackedDims, _i32, _fp, _fp, _u32, _vp, _vp, _vp,
+                                                _vp]
+    lib.retnet_state_slots_copy.argtypes = [_vp, _i64, _i64, _vp, _vp, _i64, _vp]
+    lib.retnet_slot_errors.argtypes = [ctypes.POINTER(ctypes.c_uint), _i32]
+    lib.retnet_msr_affine.argtypes = [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, ctypes.c_float, _i32, _vp]
+    lib.retnet_msr_affine_backward.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64,
+                                               ctypes.c_float, _i32, _vp, _sz, _vp]
+    lib.retnet_msr_affine_workspace_size.argtypes = [_i64, _i64, _i64, ctypes.POINTER(_sz)]
+    for name in ("retnet_retention_packed", "retnet_packed_workspace_size", "retnet_retention_step_slots",
+                 "retnet_state_slots_copy", "retnet_slot_errors", "retnet_msr_affine", "retnet_msr_affine_backward",
+                 "retnet_msr_affine_workspace_size"):
+        getattr(lib, name).restype = _i32
     lib.retnet_status_string.argtypes = [_i32]
     lib.retnet_status_string.restype = ctypes.c_char_p
     lib.retnet_version.argtypes = []
@@ -436,6 +464,187 @@ def retnet_fp16_range_errors(clear=True):
     return c.value
 
 
+# ---- serving: packed sequences over a pool of states ----------------------------------------
+
+def _one_device(*ts):
+    """All tensors on one CUDA device: that device."""
+    dev = ts[0].device
+    for t in ts:
+        if t is not None and (not t.is_cuda or t.device != dev):
+            raise ValueError("tensors must be CUDA tensors of one device")
+    return dev
+
+
+def _on(device, fn, stream):
+    """fn(raw stream) with ``device`` current (the C calls work on the current device); the stream
+    defaults to that device's current one."""
+    import torch
+    if torch.cuda.current_device() == device.index:
+        return _check(fn(_stream(stream)))
+    with torch.cuda.device(device):
+        return _check(fn(_stream(stream)))
+
+
+def _token_stride(t, name):
+    """Elements between the rows of (rows, heads, width), whose heads are contiguous."""
+    rows, heads, width = t.shape
+    sr, sh, sw = t.stride()
+    if (width > 1 and sw != 1) or (heads > 1 and sh != width) or (rows > 1 and sr < heads * width):
+        raise ValueError(f"{name}: the heads of a row must be contiguous, and rows must not overlap")
+    return sr if rows > 1 else heads * width
+
+
+def _index(t, dtype, n, name):
+    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} entries")
+    return t.data_ptr()
+
+
+def _packed_dims(q, k, v, o, pool, seqs):
+    rows, heads, dk = q.shape
+    kv, dv = v.shape[1:]
+    if tuple(k.shape) != (rows, kv, dk) or v.shape[0] != rows or tuple(o.shape) != (rows, heads, dv):
+        raise ValueError("shape mismatch between q, k, v, o")
+    if not q.dtype == k.dtype == v.dtype == o.dtype:
+        raise ValueError("q, k, v and o must have one dtype")
+    if str(pool.dtype) != "torch.float32" or pool.dim() != 4 or tuple(pool.shape[1:]) != (kv, dk, dv) or \
+            not pool.is_contiguous():
+        raise ValueError("pool must be a contiguous float32 (slots, heads_kv, d_k, d_v)")
+    return PackedDims(rows, seqs, heads, kv, dk, dv, pool.shape[0], _token_stride(q, "q"), _token_stride(k, "k"),
+                      _token_stride(v, "v"), _token_stride(o, "o"))
+
+
+def retnet_packed_workspace_size(dims) -> int:
+    """Bytes of workspace for retnet_retention_packed; dims = (tokens, seqs, heads_kv, d_k, d_v)."""
+    rows, seqs, kv, dk, dv = (int(x) for x in dims)
+    out = ctypes.c_size_t(0)
+    _check(load().retnet_packed_workspace_size(PackedDims(rows, seqs, kv, kv, dk, dv, 1), ctypes.byref(out)))
+    return out.value
+
+
+def retnet_retention_packed(q, k, v, o, pool, cu_seqlens, slots, pos, gamma, theta=None,
+                            flags=F_XPOS | F_SCALE_SQRT_D | F_NORM_D, workspace=None, stream=None):
+    """Retention over sequences packed in the token axis, into ``o`` and ``pool`` (in place).
+
+    q (T, heads, d_k), k (T, heads_kv, d_k), v (T, heads_kv, d_v), o (T, heads, d_v) of one dtype, rows
+    strided (views of a fused projection); pool (slots, heads_kv, d_k, d_v) float32; cu_seqlens
+    (seqs + 1,) int32, slots (seqs,) int32, pos (seqs,) int64 or None on the device; gamma (heads_kv,),
+    theta (d_k/2,) on the host.  Sequence i starts at position pos[i]: 0 from a zero state, else from
+    pool[slots[i]].  Without a workspace (uint8 CUDA tensor) one is allocated for the call."""
+    import torch
+    dev = _one_device(q, k, v, o, pool, cu_seqlens, slots, pos, workspace)
+    seqs = slots.shape[0]
+    d = _packed_dims(q, k, v, o, pool, seqs)
+    cu = _index(cu_seqlens, torch.int32, seqs + 1, "cu_seqlens")
+    sl = _index(slots, torch.int32, seqs, "slots")
+    ps = None if pos is None else _index(pos, torch.int64, seqs, "pos")
+    g, th = _host_f32(gamma, d.heads_kv), _host_f32(theta, d.d_k // 2)
+    if workspace is None:
+        workspace = torch.empty(retnet_packed_workspace_size((d.tokens, seqs, d.heads_kv, d.d_k, d.d_v)),
+                                dtype=torch.uint8, device=dev)
+        if stream is not None and not isinstance(stream, int):
+            workspace.record_stream(stream)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    _on(dev, lambda s: load().retnet_retention_packed(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), d, _dtype_code(q), _fptr(g), _fptr(th), int(flags), cu,
+        sl, ps, pool.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(), s), stream)
+
+
+def retnet_retention_step_slots(q, k, v, o, pool, slots, pos, gamma, theta=None,
+                                flags=F_XPOS | F_SCALE_SQRT_D | F_NORM_D, stream=None):
+    """One token for each of the rows' sequences, into ``o`` and ``pool`` (in place): q (rows, heads, d_k),
+    k (rows, heads_kv, d_k), v (rows, heads_kv, d_v), o (rows, heads, d_v); slots (rows,) int32 (negative:
+    padding) and pos (rows,) int64 or None on the device; the rest as retnet_retention_packed."""
+    import torch
+    dev = _one_device(q, k, v, o, pool, slots, pos)
+    d = _packed_dims(q, k, v, o, pool, q.shape[0])
+    sl = _index(slots, torch.int32, d.seqs, "slots")
+    ps = None if pos is None else _index(pos, torch.int64, d.seqs, "pos")
+    g, th = _host_f32(gamma, d.heads_kv), _host_f32(theta, d.d_k // 2)
+    _on(dev, lambda s: load().retnet_retention_step_slots(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), d, _dtype_code(q), _fptr(g), _fptr(th), int(flags), sl,
+        ps, pool.data_ptr(), s), stream)
+
+
+def retnet_state_slots_copy(pool, src, dst, stream=None):
+    """pool[dst[i]] <- the old pool[src[i]] for all pairs at once (zeros where src[i] < 0; dst[i] < 0 is
+    padding): pool (slots, ...) float32, src and dst (pairs,) int32 on the device, up to MAX_SLOT_PAIRS."""
+    import torch
+    dev = _one_device(pool, src, dst)
+    if pool.dtype != torch.float32 or not pool.is_contiguous():
+        raise ValueError("pool must be a contiguous float32 tensor")
+    n = src.shape[0]
+    sp, dp = _index(src, torch.int32, n, "src"), _index(dst, torch.int32, n, "dst")
+    slots = pool.shape[0]
+    _on(dev, lambda s: load().retnet_state_slots_copy(pool.data_ptr(), slots, pool.numel() // max(slots, 1), sp, dp, n,
+                                                      s), stream)
+
+
+def retnet_slot_errors(clear=True):
+    """Sequences, rows and pairs that the three calls above left out because their slots, positions or
+    cu_seqlens were wrong, since the last clear (synchronises)."""
+    c = ctypes.c_uint(0)
+    _check(load().retnet_slot_errors(ctypes.byref(c), 1 if clear else 0))
+    return c.value
+
+
+# ---- the MSR epilogue with a learnable affine ------------------------------------------------
+
+def _msr_args(y, weight, bias, *same):
+    import torch
+    if y.dim() != 3:
+        raise ValueError("y must be (tokens, heads, d_v)")
+    for t in (y, *same):
+        if t.shape != y.shape or t.dtype != y.dtype or not t.is_contiguous():
+            raise ValueError("y, g, out, dout, dy and dg must be contiguous and have one shape and dtype")
+    for t in (weight, bias):
+        if t is not None and (tuple(t.shape) != tuple(y.shape[1:]) or t.dtype != torch.float32 or not t.is_contiguous()):
+            raise ValueError("weight, bias, dweight and dbias must be contiguous float32 (heads, d_v)")
+    return _one_device(y, weight, bias, *same)
+
+
+def _optional_ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def retnet_msr_affine(y, g, weight, bias, out, eps=1e-5, stream=None):
+    """swish(g) * (weight * GroupNorm_h(y) + bias) into ``out``: y, g, out (tokens, heads, d_v) of one dtype,
+    weight and bias (heads, d_v) float32 or None."""
+    dev = _msr_args(y, weight, bias, g, out)
+    _on(dev, lambda s: load().retnet_msr_affine(y.data_ptr(), g.data_ptr(), _optional_ptr(weight), _optional_ptr(bias),
+                                                out.data_ptr(), *y.shape, float(eps), _dtype_code(y), s), stream)
+
+
+def retnet_msr_affine_workspace_size(shape) -> int:
+    """Bytes of workspace for retnet_msr_affine_backward; shape = (tokens, heads, d_v)."""
+    out = ctypes.c_size_t(0)
+    _check(load().retnet_msr_affine_workspace_size(*(int(x) for x in shape), ctypes.byref(out)))
+    return out.value
+
+
+def retnet_msr_affine_backward(y, g, weight, bias, dout, dy, dg, dweight=None, dbias=None, eps=1e-5, workspace=None,
+                               stream=None):
+    """Gradient of retnet_msr_affine into dy, dg (shape and dtype of y) and, where given, dweight and dbias
+    (heads, d_v) float32.  Without a workspace (uint8 CUDA tensor) one is allocated for the call."""
+    import torch
+    dev = _msr_args(y, weight, bias, g, dout, dy, dg)
+    _msr_args(y, dweight, dbias)
+    if workspace is None and (dweight is not None or dbias is not None):
+        workspace = torch.empty(retnet_msr_affine_workspace_size(y.shape), dtype=torch.uint8, device=dev)
+        if stream is not None and not isinstance(stream, int):
+            workspace.record_stream(stream)
+    elif workspace is not None:
+        _one_device(y, workspace)
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _on(dev, lambda s: load().retnet_msr_affine_backward(
+        y.data_ptr(), g.data_ptr(), _optional_ptr(weight), _optional_ptr(bias), dout.data_ptr(), dy.data_ptr(),
+        dg.data_ptr(), _optional_ptr(dweight), _optional_ptr(dbias), *y.shape, float(eps), _dtype_code(y),
+        _optional_ptr(workspace), ws_bytes, s), stream)
+
+
 # ---- allocating conveniences (torch.empty for the outputs, then the calls above) ----------
 
 def retention_chunkwise(q, k, v, gamma, theta=None, chunk=64, flags=F_ALL, pos0=0, out_dtype=None,
@@ -454,3 +663,19 @@ def retention_parallel(q, k, v, gamma, theta=None, flags=F_ALL, pos0=0, out_dtyp
     o = torch.empty(v.shape, dtype=out_dtype or v.dtype, device=v.device)
     retnet_retention_parallel(q, k, v, o, gamma, theta, pos0, flags, stream)
     return o
+
+
+def msr_affine(y, g, weight=None, bias=None, eps=1e-5, stream=None):
+    import torch
+    out = torch.empty_like(y)
+    retnet_msr_affine(y, g, weight, bias, out, eps, stream)
+    return out
+
+
+def msr_affine_backward(y, g, weight, bias, dout, eps=1e-5, workspace=None, stream=None):
+    """(dy, dg, dweight, dbias) of msr_affine."""
+    import torch
+    dy, dg = torch.empty_like(y), torch.empty_like(g)
+    dw, db = (torch.empty(y.shape[1:], dtype=torch.float32, device=y.device) for _ in range(2))
+    retnet_msr_affine_backward(y, g, weight, bias, dout, dy, dg, dw, db, eps, workspace, stream)
+    return dy, dg, dw, db

@@ -45,6 +45,17 @@ __device__ __forceinline__ void xpos_sincos(int64_t p, float theta, float* s, fl
   sincosf(static_cast<float>(a), s, c);
 }
 
+// The same for any position below 2^53: the product p * theta exactly (its rounding error by one
+// fma) and 2 pi in two parts, so that the angle keeps fp32 accuracy where p * theta * 2^-53 alone
+// passes it (p * theta above about 2^29).
+__device__ __forceinline__ void position_sincos(int64_t p, float theta, float* s, float* c) {
+  const double two_pi = 6.283185307179586476925286766559, two_pi_low = 2.4492935982947064e-16;
+  const double x = static_cast<double>(p), t = static_cast<double>(theta);
+  const double a = x * t, low = fma(x, t, -a);
+  const double n = rint(a * 0.15915494309189533577);
+  sincosf(static_cast<float>(fma(-n, two_pi, a) + fma(-n, two_pi_low, low)), s, c);
+}
+
 // Per-row output factor of the normalisations ("阅读笔记：RetNet" §三.3):
 //   s / c_p,  s = 1/sqrt(d_k) with RETNET_F_SCALE_SQRT_D,
 //   c_p = sqrt(sum_{j=0..p} gamma^j) = sqrt((1 - gamma^(p+1)) / (1 - gamma)) with RETNET_F_NORM_D.

@@ -139,4 +139,52 @@ cudaError_t launch_msr_epilogue(const void* y, const void* g, void* out, int64_t
                                 int64_t d_v, float eps, retnet_dtype_t in_dtype, retnet_dtype_t out_dtype,
                                 cudaStream_t s);
 
+// ---- packed sequences over a pool of states -------------------------------------------------
+// One call of retnet_retention_packed, after host validation.  Strides are in elements between
+// the rows of consecutive tokens; the heads of a row are contiguous.
+struct PackedCall {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* o;
+  int64_t rows, seqs, heads, heads_kv, d_k, d_v, slots;
+  int64_t stride_q, stride_k, stride_v, stride_o;
+  retnet_dtype_t dtype;
+  uint32_t flags;
+  const int32_t* cu;
+  const int32_t* slot;
+  const int64_t* pos;
+  float* pool;
+  void* ws;
+  size_t ws_bytes;
+};
+// Bytes of workspace a call needs on either path.
+size_t packed_workspace_bytes(int64_t rows, int64_t seqs, int64_t heads_kv, int64_t d_k, int64_t d_v);
+cudaError_t launch_packed_simt(const PackedCall& c, const HeadParams& hp, cudaStream_t s);
+
+// One token for each of rows sequences (retnet_retention_step_slots): rows == seqs, cu unused.
+cudaError_t launch_step_slots(const PackedCall& c, const HeadParams& hp, cudaStream_t s);
+// pool[dst[i]] <- the old pool[src[i]] (zeros where src[i] < 0).
+cudaError_t launch_slots_copy(float* pool, int64_t slots, int64_t slot_floats, const int32_t* src, const int32_t* dst,
+                              int64_t n, cudaStream_t s);
+// Reads (and optionally clears) the counts of rows, sequences and pairs refused on the device.
+cudaError_t packed_index_errors(unsigned int* count, bool clear);
+cudaError_t step_index_errors(unsigned int* count, bool clear);
+cudaError_t slots_index_errors(unsigned int* count, bool clear);
+
+// MSR epilogue with a learnable affine, and its gradient.
+struct MsrAffineCall {
+  const void* y;
+  const void* g;
+  const float* weight;  // [heads][d_v] or nullptr (ones)
+  const float* bias;    // [heads][d_v] or nullptr (zeros)
+  int64_t tokens, heads, d_v;
+  float eps;
+  retnet_dtype_t dtype;
+};
+cudaError_t launch_msr_affine(const MsrAffineCall& c, void* out, cudaStream_t s);
+size_t msr_backward_workspace_bytes(int64_t tokens, int64_t heads, int64_t d_v);
+cudaError_t launch_msr_affine_backward(const MsrAffineCall& c, const void* dout, void* dy, void* dg, float* dweight,
+                                       float* dbias, void* ws, cudaStream_t s);
+
 }  // namespace retnet

@@ -1,0 +1,39 @@
+// packed.cuh -- retention over sequences packed in one token axis: what its kernels share.
+//
+// A call's sequences are ragged and their lengths live on the device, so the host cannot plan the
+// work.  It cuts every sequence into runs of `run` tokens and gives the grids room for the most
+// runs there can be: sequence s owns the units from cu_seqlens[s] / run + s on.  Those first units
+// grow by at least ceil(len / run) from one sequence to the next (floor(a + len) - floor(a) + 1 >=
+// ceil(len) in units of run), so no two sequences share a unit, the last unit is below
+// tokens / run + seqs, and a unit finds its sequence by counting, without a prefix sum over the
+// lengths.  launch_packed_plan writes one descriptor a unit (tokens 0 where it has no work).
+#pragma once
+
+#include "launch.h"
+
+namespace retnet {
+
+struct RunDesc {
+  int32_t seq;     // its sequence
+  int32_t row;     // first row of the run in q, k, v, o
+  int32_t tokens;  // rows of the run; 0: nothing to do
+  int32_t index;   // the run's place in its sequence
+  int32_t runs;    // runs of the sequence
+  int32_t slot;    // the sequence's pool slot
+  int64_t pos;     // absolute position of the run's first token
+};
+
+struct PackedIndex {
+  const int32_t* cu;   // [seqs + 1]
+  const int32_t* slots;  // [seqs]
+  const int64_t* pos;  // [seqs] or nullptr (all 0)
+  int64_t rows;        // rows of q, k, v, o
+  int32_t seqs, n_slots, run;
+};
+
+inline int64_t packed_units(int64_t rows, int64_t seqs, int64_t run) { return rows / run + seqs; }
+
+// Writes desc[0 .. packed_units).
+cudaError_t launch_packed_plan(const PackedIndex& ix, RunDesc* desc, cudaStream_t s);
+
+}  // namespace retnet

@@ -520,4 +520,166 @@ retnet_status_t retnet_msr_epilogue(const void* y, const void* g, void* out, int
                                        static_cast<cudaStream_t>(stream)));
 }
 
+// ---- packed sequences, state slots, affine MSR epilogue --------------------------------------
+
+namespace {
+bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// What the packed call and its single-token form check alike; seqs: entries of slots and pos.
+retnet_status_t check_packed(const retnet_packed_t& d, retnet_dtype_t dtype, uint32_t flags) {
+  if (!valid_dtype(dtype)) return RETNET_ERR_BAD_DTYPE;
+  if (d.tokens < 0 || d.tokens > 0x7fffffffLL || d.seqs < 0 || d.seqs > 65535) return RETNET_ERR_BAD_SHAPE;
+  if (d.heads <= 0 || d.heads > RETNET_MAX_HEADS || d.heads_kv <= 0 || d.heads % d.heads_kv) return RETNET_ERR_BAD_SHAPE;
+  if (d.d_k <= 0 || d.d_k > RETNET_MAX_DK || d.d_v <= 0 || d.d_v > RETNET_MAX_DV) return RETNET_ERR_BAD_SHAPE;
+  if (d.slots <= 0 || d.slots > 0x7fffffffLL) return RETNET_ERR_BAD_SHAPE;
+  if (d.stride_q < d.heads * d.d_k || d.stride_k < d.heads_kv * d.d_k || d.stride_v < d.heads_kv * d.d_v ||
+      d.stride_o < d.heads * d.d_v)
+    return RETNET_ERR_BAD_SHAPE;
+  if (flags & ~kAllFlags) return RETNET_ERR_BAD_PARAM;
+  if ((flags & RETNET_F_XPOS) && (d.d_k & 1)) return RETNET_ERR_BAD_PARAM;
+  if (flags & RETNET_F_NORM_R) return RETNET_ERR_UNSUPPORTED;
+  return RETNET_OK;
+}
+retnet_status_t check_packed_pointers(const PackedCall& c) {
+  if (!c.q || !c.k || !c.v || !c.o || !c.slot || !c.pool) return RETNET_ERR_NULL_PTR;
+  const uintptr_t el = c.dtype == RETNET_F32 ? 4 : 2;
+  if (!aligned_to(c.q, el) || !aligned_to(c.k, el) || !aligned_to(c.v, el) || !aligned_to(c.o, el) ||
+      !aligned_to(c.slot, 4) || !aligned_to(c.pos, 8) || !aligned16(c.pool))
+    return RETNET_ERR_BAD_PARAM;
+  return RETNET_OK;
+}
+PackedCall packed_call(const void* q, const void* k, const void* v, void* o, const retnet_packed_t& d,
+                       retnet_dtype_t dtype, uint32_t flags, const int32_t* cu, const int32_t* slots, const int64_t* pos,
+                       float* pool) {
+  return PackedCall{q, k, v, o, d.tokens, d.seqs, d.heads, d.heads_kv, d.d_k, d.d_v, d.slots, d.stride_q, d.stride_k,
+                    d.stride_v, d.stride_o, dtype, flags, cu, slots, pos, pool, nullptr, 0};
+}
+}  // namespace
+
+retnet_status_t retnet_packed_workspace_size(retnet_packed_t dims, size_t* bytes) {
+  if (!bytes) return RETNET_ERR_NULL_PTR;
+  if (dims.tokens < 0 || dims.seqs < 0 || dims.heads_kv < 0 || dims.d_k < 0 || dims.d_v < 0) return RETNET_ERR_BAD_SHAPE;
+  *bytes = packed_workspace_bytes(dims.tokens, dims.seqs, dims.heads_kv, dims.d_k, dims.d_v);
+  return RETNET_OK;
+}
+
+retnet_status_t retnet_retention_packed(const void* q, const void* k, const void* v, void* o, retnet_packed_t dims,
+                                        retnet_dtype_t dtype, const float* gamma, const float* theta, uint32_t flags,
+                                        const int32_t* cu_seqlens, const int32_t* slots, const int64_t* pos, float* pool,
+                                        void* workspace, size_t workspace_bytes, void* stream) {
+  retnet_status_t st = check_packed(dims, dtype, flags);
+  if (st != RETNET_OK) return st;
+  HeadParams hp;
+  if ((st = fill_params(&hp, gamma, theta, dims.heads_kv, dims.d_k, flags)) != RETNET_OK) return st;
+  if (dims.tokens == 0 || dims.seqs == 0) return RETNET_OK;
+  PackedCall c = packed_call(q, k, v, o, dims, dtype, flags, cu_seqlens, slots, pos, pool);
+  if ((st = check_packed_pointers(c)) != RETNET_OK) return st;
+  if (!cu_seqlens || !workspace) return RETNET_ERR_NULL_PTR;
+  if (!aligned_to(cu_seqlens, 4) || !aligned16(workspace) ||
+      workspace_bytes < packed_workspace_bytes(c.rows, c.seqs, c.heads_kv, c.d_k, c.d_v))
+    return RETNET_ERR_BAD_PARAM;
+  if ((st = check_device()) != RETNET_OK) return st;
+  c.ws = workspace;
+  c.ws_bytes = workspace_bytes;
+  return from_cuda(launch_packed_simt(c, hp, static_cast<cudaStream_t>(stream)));
+}
+
+retnet_status_t retnet_retention_step_slots(const void* q, const void* k, const void* v, void* o, retnet_packed_t dims,
+                                            retnet_dtype_t dtype, const float* gamma, const float* theta, uint32_t flags,
+                                            const int32_t* slots, const int64_t* pos, float* pool, void* stream) {
+  retnet_status_t st = check_packed(dims, dtype, flags);
+  if (st != RETNET_OK) return st;
+  if (dims.tokens != dims.seqs) return RETNET_ERR_BAD_SHAPE;
+  HeadParams hp;
+  if ((st = fill_params(&hp, gamma, theta, dims.heads_kv, dims.d_k, flags)) != RETNET_OK) return st;
+  if (dims.seqs == 0) return RETNET_OK;
+  const PackedCall c = packed_call(q, k, v, o, dims, dtype, flags, nullptr, slots, pos, pool);
+  if ((st = check_packed_pointers(c)) != RETNET_OK) return st;
+  if ((st = check_device()) != RETNET_OK) return st;
+  return from_cuda(launch_step_slots(c, hp, static_cast<cudaStream_t>(stream)));
+}
+
+retnet_status_t retnet_state_slots_copy(float* pool, int64_t slots, int64_t slot_floats, const int32_t* src,
+                                        const int32_t* dst, int64_t pairs, void* stream) {
+  if (slots <= 0 || slots > 0x7fffffffLL || slot_floats <= 0 || pairs < 0 || pairs > RETNET_MAX_SLOT_PAIRS)
+    return RETNET_ERR_BAD_SHAPE;
+  if (pairs == 0) return RETNET_OK;
+  if (!pool || !src || !dst) return RETNET_ERR_NULL_PTR;
+  if (!aligned16(pool) || !aligned_to(src, 4) || !aligned_to(dst, 4)) return RETNET_ERR_BAD_PARAM;
+  const retnet_status_t st = check_device();
+  if (st != RETNET_OK) return st;
+  return from_cuda(launch_slots_copy(pool, slots, slot_floats, src, dst, pairs, static_cast<cudaStream_t>(stream)));
+}
+
+retnet_status_t retnet_slot_errors(unsigned int* count, int clear) {
+  if (!count) return RETNET_ERR_NULL_PTR;
+  if (cudaDeviceSynchronize() != cudaSuccess) return RETNET_ERR_CUDA;
+  unsigned int n[3] = {0, 0, 0};
+  if (packed_index_errors(&n[0], clear != 0) != cudaSuccess || step_index_errors(&n[1], clear != 0) != cudaSuccess ||
+      slots_index_errors(&n[2], clear != 0) != cudaSuccess)
+    return RETNET_ERR_CUDA;
+  *count = n[0] + n[1] + n[2];
+  return RETNET_OK;
+}
+
+namespace {
+retnet_status_t check_msr_affine(const MsrAffineCall& c) {
+  if (!valid_dtype(c.dtype)) return RETNET_ERR_BAD_DTYPE;
+  if (c.tokens < 0 || c.heads <= 0 || c.heads > 65535 || c.d_v <= 0 || c.d_v > RETNET_MAX_DV) return RETNET_ERR_BAD_SHAPE;
+  if (c.tokens > 0x7fffffffLL || c.tokens * c.heads > 0x7fffffffLL) return RETNET_ERR_BAD_SHAPE;
+  if (!(c.eps >= 0.f) || !isfinite(c.eps)) return RETNET_ERR_BAD_PARAM;
+  const uintptr_t el = c.dtype == RETNET_F32 ? 4 : 2;
+  if (!aligned_to(c.y, el) || !aligned_to(c.g, el) || !aligned_to(c.weight, 4) || !aligned_to(c.bias, 4))
+    return RETNET_ERR_BAD_PARAM;
+  return RETNET_OK;
+}
+}  // namespace
+
+retnet_status_t retnet_msr_affine(const void* y, const void* g, const float* weight, const float* bias, void* out,
+                                  int64_t tokens, int64_t heads, int64_t d_v, float eps, retnet_dtype_t dtype,
+                                  void* stream) {
+  const MsrAffineCall c{y, g, weight, bias, tokens, heads, d_v, eps, dtype};
+  retnet_status_t st = check_msr_affine(c);
+  if (st != RETNET_OK) return st;
+  if (tokens == 0) return RETNET_OK;
+  if (!y || !g || !out) return RETNET_ERR_NULL_PTR;
+  if (!aligned_to(out, dtype == RETNET_F32 ? 4 : 2)) return RETNET_ERR_BAD_PARAM;
+  if ((st = check_device()) != RETNET_OK) return st;
+  return from_cuda(launch_msr_affine(c, out, static_cast<cudaStream_t>(stream)));
+}
+
+retnet_status_t retnet_msr_affine_workspace_size(int64_t tokens, int64_t heads, int64_t d_v, size_t* bytes) {
+  if (!bytes) return RETNET_ERR_NULL_PTR;
+  if (tokens < 0 || heads <= 0 || d_v <= 0) return RETNET_ERR_BAD_SHAPE;
+  *bytes = msr_backward_workspace_bytes(tokens, heads, d_v);
+  return RETNET_OK;
+}
+
+retnet_status_t retnet_msr_affine_backward(const void* y, const void* g, const float* weight, const float* bias,
+                                           const void* dout, void* dy, void* dg, float* dweight, float* dbias,
+                                           int64_t tokens, int64_t heads, int64_t d_v, float eps, retnet_dtype_t dtype,
+                                           void* workspace, size_t workspace_bytes, void* stream) {
+  const MsrAffineCall c{y, g, weight, bias, tokens, heads, d_v, eps, dtype};
+  retnet_status_t st = check_msr_affine(c);
+  if (st != RETNET_OK) return st;
+  if (!aligned_to(dweight, 4) || !aligned_to(dbias, 4)) return RETNET_ERR_BAD_PARAM;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (tokens == 0) {  // empty sums
+    const size_t bytes = sizeof(float) * static_cast<size_t>(heads * d_v);
+    if (dweight && cudaMemsetAsync(dweight, 0, bytes, s) != cudaSuccess) return RETNET_ERR_CUDA;
+    if (dbias && cudaMemsetAsync(dbias, 0, bytes, s) != cudaSuccess) return RETNET_ERR_CUDA;
+    return RETNET_OK;
+  }
+  if (!y || !g || !dout || !dy || !dg) return RETNET_ERR_NULL_PTR;
+  const uintptr_t el = dtype == RETNET_F32 ? 4 : 2;
+  if (!aligned_to(dout, el) || !aligned_to(dy, el) || !aligned_to(dg, el)) return RETNET_ERR_BAD_PARAM;
+  if (dweight || dbias) {
+    if (!workspace) return RETNET_ERR_NULL_PTR;
+    if (!aligned16(workspace) || workspace_bytes < msr_backward_workspace_bytes(tokens, heads, d_v))
+      return RETNET_ERR_BAD_PARAM;
+  }
+  if ((st = check_device()) != RETNET_OK) return st;
+  return from_cuda(launch_msr_affine_backward(c, dout, dy, dg, dweight, dbias, workspace, s));
+}
+
 }  // extern "C"

@@ -1,0 +1,143 @@
+"""Refusals of the packed, single-token, slot-copy and affine-MSR entry points (no GPU needed): each
+bad argument gets its documented status before any device is touched."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import linear_attention_sequence_chunkwise_b200 as rn
+from linear_attention_sequence_chunkwise_b200 import _build
+
+FAKE = 0x10000  # never dereferenced
+
+
+@pytest.fixture(scope="module")
+def lib():
+    _build.build()
+    return rn.load()
+
+
+def _fp(a):
+    return a.ctypes.data_as(rn._fp)
+
+
+def _dims(**kw):
+    d = dict(tokens=10, seqs=2, heads=4, heads_kv=2, d_k=16, d_v=8, slots=5, stride_q=64, stride_k=32, stride_v=16,
+             stride_o=32)
+    d.update(kw)
+    return rn.PackedDims(**d)
+
+
+G2, TH8 = np.full(2, 0.9, np.float32), np.ones(8, np.float32)
+BIG = 1 << 40
+
+
+def _packed(lib, d=None, q=FAKE, o=FAKE, dtype=0, gamma=G2, theta=TH8, flags=rn.F_XPOS, cu=FAKE, slots=FAKE, pos=FAKE,
+            pool=FAKE, ws=FAKE, ws_bytes=BIG):
+    return lib.retnet_retention_packed(q, FAKE, FAKE, o, d or _dims(), dtype, _fp(gamma),
+                                       None if theta is None else _fp(theta), flags, cu, slots, pos, pool, ws, ws_bytes,
+                                       None)
+
+
+def _step(lib, d=None, dtype=0, flags=0, slots=FAKE, pos=FAKE, pool=FAKE, gamma=G2):
+    return lib.retnet_retention_step_slots(FAKE, FAKE, FAKE, FAKE, d or _dims(tokens=2), dtype, _fp(gamma), None, flags,
+                                           slots, pos, pool, None)
+
+
+BAD_DIMS = [dict(tokens=-1), dict(tokens=1 << 31), dict(seqs=-1), dict(seqs=65536), dict(heads=0), dict(heads_kv=0),
+            dict(heads=3), dict(heads=258, stride_q=1 << 20, stride_o=1 << 20), dict(d_k=0), dict(d_v=0),
+            dict(d_k=514, stride_q=1 << 20, stride_k=1 << 20), dict(d_v=1025, stride_v=1 << 20, stride_o=1 << 20),
+            dict(slots=0), dict(stride_q=63), dict(stride_k=31), dict(stride_v=15), dict(stride_o=31)]
+
+
+@pytest.mark.parametrize("bad", BAD_DIMS)
+def test_packed_shapes(lib, bad):
+    assert _packed(lib, _dims(**bad)) == 2
+    assert _step(lib, _dims(**{"tokens": 2, **bad})) == 2
+
+
+def test_packed_refusals(lib):
+    assert _packed(lib, dtype=2) == 3
+    assert _packed(lib, flags=64) == 4
+    assert _packed(lib, flags=rn.F_NORM_R) == 5
+    assert _packed(lib, _dims(d_k=15, stride_q=60), flags=rn.F_XPOS) == 4  # odd d_k with xPos
+    assert _packed(lib, gamma=np.array([0.9, 1.0], np.float32)) == 4
+    assert _packed(lib, theta=None) == 1
+    assert _packed(lib, theta=np.full(8, np.inf, np.float32)) == 4
+    for name in ("q", "o", "cu", "slots", "pool", "ws"):
+        assert _packed(lib, **{name: None}) == 1, name
+    assert _packed(lib, q=FAKE + 2) == 4 and _packed(lib, q=FAKE + 1, dtype=1) == 4
+    assert _packed(lib, cu=FAKE + 2) == 4 and _packed(lib, slots=FAKE + 2) == 4 and _packed(lib, pos=FAKE + 4) == 4
+    assert _packed(lib, pool=FAKE + 4) == 4 and _packed(lib, ws=FAKE + 8) == 4
+    n = rn.retnet_packed_workspace_size((10, 2, 2, 16, 8))
+    assert n > 0 and _packed(lib, ws_bytes=n - 1) == 4
+    assert _packed(lib, _dims(tokens=0), q=None) == 0 and _packed(lib, _dims(seqs=0), cu=None) == 0  # no work
+
+
+def test_step_refusals(lib):
+    assert _step(lib, _dims(tokens=3)) == 2  # tokens != seqs
+    assert _step(lib, dtype=5) == 3
+    assert _step(lib, flags=rn.F_NORM_R) == 5
+    assert _step(lib, slots=None) == 1 and _step(lib, pool=None) == 1
+    assert _step(lib, pool=FAKE + 8) == 4 and _step(lib, pos=FAKE + 4) == 4
+    assert _step(lib, _dims(tokens=0, seqs=0), slots=None) == 0
+
+
+def test_slots_copy_refusals(lib):
+    def call(pool=FAKE, slots=4, floats=16, src=FAKE, dst=FAKE, n=2):
+        return lib.retnet_state_slots_copy(pool, slots, floats, src, dst, n, None)
+    assert call(slots=0) == 2 and call(floats=0) == 2 and call(n=-1) == 2 and call(n=rn.MAX_SLOT_PAIRS + 1) == 2
+    assert call(pool=None) == 1 and call(src=None) == 1 and call(dst=None) == 1
+    assert call(pool=FAKE + 4) == 4 and call(src=FAKE + 2) == 4
+    assert call(n=0, pool=None) == 0
+
+
+def test_msr_affine_refusals(lib):
+    def fwd(y=FAKE, g=FAKE, w=FAKE, out=FAKE, tokens=3, heads=2, dv=8, eps=1e-5, dtype=0):
+        return lib.retnet_msr_affine(y, g, w, None, out, tokens, heads, dv, eps, dtype, None)
+
+    def bwd(dout=FAKE, dy=FAKE, dw=FAKE, ws=FAKE, n=BIG, tokens=3, heads=2, dv=8, eps=1e-5, dtype=0):
+        return lib.retnet_msr_affine_backward(FAKE, FAKE, None, None, dout, dy, FAKE, dw, None, tokens, heads, dv, eps,
+                                              dtype, ws, n, None)
+    for f in (fwd, bwd):
+        assert f(dtype=3) == 3 and f(tokens=-1) == 2 and f(heads=0) == 2 and f(dv=0) == 2 and f(dv=1025) == 2
+        assert f(tokens=1 << 30, heads=4) == 2
+        assert f(eps=-1.0) == 4 and f(eps=float("nan")) == 4
+    assert fwd(y=None) == 1 and fwd(out=None) == 1 and fwd(y=FAKE + 2) == 4 and fwd(y=FAKE + 1, dtype=1) == 4
+    assert fwd(w=FAKE + 2) == 4 and fwd(tokens=0, y=None) == 0
+    assert bwd(dout=None) == 1 and bwd(dy=None) == 1 and bwd(ws=None) == 1 and bwd(ws=FAKE + 4) == 4
+    need = rn.retnet_msr_affine_workspace_size((3, 2, 8))
+    assert bwd(n=need - 1) == 4
+
+
+def test_binding_refusals():
+    """Wrong shapes, types, layouts and host tensors raise before the library is called."""
+    q, k, v, o = torch.zeros(4, 4, 16), torch.zeros(4, 2, 16), torch.zeros(4, 2, 8), torch.zeros(4, 4, 8)
+    pool, cu = torch.zeros(5, 2, 16, 8), torch.zeros(3, dtype=torch.int32)
+    sl, pos = torch.zeros(2, dtype=torch.int32), torch.zeros(2, dtype=torch.int64)
+    with pytest.raises(ValueError, match="CUDA tensors"):
+        rn.retnet_retention_packed(q, k, v, o, pool, cu, sl, pos, G2, TH8)
+    d = rn._packed_dims(q, k, v, o, pool, 2)
+    assert (d.tokens, d.seqs, d.heads, d.heads_kv, d.d_k, d.d_v, d.slots, d.stride_q) == (4, 2, 4, 2, 16, 8, 5, 64)
+    wide = torch.zeros(4, 200)
+    assert rn._token_stride(wide[:, 3:67].unflatten(1, (4, 16)), "q") == 200
+    with pytest.raises(ValueError, match="heads of a row"):
+        rn._token_stride(torch.zeros(4, 16, 4).transpose(1, 2), "q")
+    with pytest.raises(ValueError, match="rows must not overlap"):
+        rn._token_stride(torch.zeros(1, 4, 16).expand(4, 4, 16), "q")
+    with pytest.raises(ValueError, match="shape mismatch"):
+        rn._packed_dims(q, k[:, :1], v, o, pool, 2)
+    with pytest.raises(ValueError, match="one dtype"):
+        rn._packed_dims(q, k, v, o.bfloat16(), pool, 2)
+    with pytest.raises(ValueError, match="pool"):
+        rn._packed_dims(q, k, v, o, pool.double(), 2)
+    with pytest.raises(ValueError, match="cu_seqlens"):
+        rn._index(cu.long(), torch.int32, 3, "cu_seqlens")
+    with pytest.raises(ValueError, match="slots"):
+        rn._index(sl, torch.int32, 3, "slots")
+    y = torch.zeros(3, 2, 8)
+    with pytest.raises(ValueError, match="one shape"):
+        rn._msr_args(y, None, None, y[:, :, :4])
+    with pytest.raises(ValueError, match="float32"):
+        rn._msr_args(y, torch.zeros(8), None, y)
