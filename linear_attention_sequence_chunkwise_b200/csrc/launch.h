@@ -158,8 +158,15 @@ struct PackedCall {
   void* ws;
   size_t ws_bytes;
 };
-// Bytes of workspace a call needs on either path.
-size_t packed_workspace_bytes(int64_t rows, int64_t seqs, int64_t heads_kv, int64_t d_k, int64_t d_v);
+// The tensor-core kernels take this call: bf16, d_k 64, 128 or 256, d_v a multiple of 64, rows and
+// pointers on 16-byte boundaries, gamma^128 >= 2^-12 for every head, no RETNET_F_PRECISE.
+bool packed_tc_supported(const PackedCall& c, const HeadParams& hp);
+// Bytes of workspace of the two kernel families.
+size_t packed_simt_workspace_bytes(int64_t rows, int64_t seqs, int64_t heads_kv, int64_t d_k, int64_t d_v);
+size_t packed_tc_workspace_bytes(int64_t rows, int64_t seqs, int64_t heads_kv, int64_t d_k, int64_t d_v);
+cudaError_t launch_packed_tc(const PackedCall& c, const HeadParams& hp, cudaStream_t s);
+cudaError_t packed_wait_timeouts(unsigned int* count, bool clear);
+cudaError_t packed_fp16_overflows(unsigned int* count, bool clear);
 cudaError_t launch_packed_simt(const PackedCall& c, const HeadParams& hp, cudaStream_t s);
 
 // One token for each of rows sequences (retnet_retention_step_slots): rows == seqs, cu unused.

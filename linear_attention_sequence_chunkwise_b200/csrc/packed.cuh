@@ -33,7 +33,17 @@ struct PackedIndex {
 
 inline int64_t packed_units(int64_t rows, int64_t seqs, int64_t run) { return rows / run + seqs; }
 
-// Writes desc[0 .. packed_units).
-cudaError_t launch_packed_plan(const PackedIndex& ix, RunDesc* desc, cudaStream_t s);
+// The rotation of a token is base x offset (complex products): base[unit][i][j] turns pair j by the
+// angle of the run's token 16 i, offset[r][j] by that of r further tokens, so that a kernel needs no
+// sine or cosine of its own.  base: [units][run / 16][half], offset: [16][half]; nullptr: not written.
+struct PackedRotation {
+  float2* base;
+  float2* offset;
+  int half;
+  bool xpos;
+};
+// Writes desc[0 .. packed_units) and the rotations.
+cudaError_t launch_packed_plan(const PackedIndex& ix, RunDesc* desc, const PackedRotation& rot, const HeadParams& hp,
+                               cudaStream_t s);
 
 }  // namespace retnet

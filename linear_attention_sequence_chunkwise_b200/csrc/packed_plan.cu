@@ -10,11 +10,18 @@ constexpr int kThreads = 128;
 
 __device__ unsigned int g_packed_errors = 0;
 
+__device__ __forceinline__ float2 turn(const PackedRotation& rot, int64_t p, int j, const HeadParams& hp) {
+  float s = 0.f, c = 1.f;
+  if (rot.xpos) position_sincos(p, hp.theta[j], &s, &c);
+  return make_float2(c, s);
+}
+
 // One CTA a unit.  The sequence of a unit is the last one whose first unit is not behind it.  A call
 // whose cu_seqlens is out of order or leaves the rows has no runs; a sequence is refused (no run)
 // when its slot is out of range or an earlier sequence with tokens has it, or its position is
 // negative; one with slot < 0 or no tokens has none either.
-__global__ void __launch_bounds__(kThreads) plan_kernel(PackedIndex ix, RunDesc* __restrict__ desc) {
+__global__ void __launch_bounds__(kThreads) plan_kernel(PackedIndex ix, RunDesc* __restrict__ desc, PackedRotation rot,
+                                                        HeadParams hp) {
   const int tid = threadIdx.x;
   const int64_t u = blockIdx.x;
   int bad = 0, before = 0;
@@ -44,8 +51,12 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PackedIndex ix, RunDesc*
     for (int j = tid; j < s; j += kThreads) dup |= ix.slots[j] == slot && ix.cu[j + 1] > ix.cu[j];
   }
   dup = __syncthreads_or(dup);
-  if (tid != 0) return;
-  if (s >= 0) {
+  __shared__ int64_t first;  // the run's position, -1 without a run
+  if (tid == 0) first = -1;
+  if (rot.offset && u == 0) {
+    for (int e = tid; e < 16 * rot.half; e += kThreads) rot.offset[e] = turn(rot, e / rot.half, e % rot.half, hp);
+  }
+  if (tid == 0 && s >= 0) {
     const int64_t a = ix.cu[s], len = ix.cu[s + 1] - a, pos = ix.pos ? ix.pos[s] : 0;
     const int32_t slot = ix.slots[s];
     const int64_t i = u - (a / ix.run + s), runs = (len + ix.run - 1) / ix.run;
@@ -61,16 +72,24 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PackedIndex ix, RunDesc*
         d.runs = static_cast<int32_t>(runs);
         d.slot = slot;
         d.pos = pos + i * ix.run;
+        first = d.pos;
       }
     }
   }
-  desc[u] = d;
+  if (tid == 0) desc[u] = d;
+  if (!rot.base) return;
+  __syncthreads();
+  if (first < 0) return;
+  const int n = ix.run / 16 * rot.half;
+  for (int e = tid; e < n; e += kThreads)
+    rot.base[u * n + e] = turn(rot, first + 16 * (e / rot.half), e % rot.half, hp);
 }
 
 }  // namespace
 
-cudaError_t launch_packed_plan(const PackedIndex& ix, RunDesc* desc, cudaStream_t s) {
-  plan_kernel<<<static_cast<unsigned>(packed_units(ix.rows, ix.seqs, ix.run)), kThreads, 0, s>>>(ix, desc);
+cudaError_t launch_packed_plan(const PackedIndex& ix, RunDesc* desc, const PackedRotation& rot, const HeadParams& hp,
+                               cudaStream_t s) {
+  plan_kernel<<<static_cast<unsigned>(packed_units(ix.rows, ix.seqs, ix.run)), kThreads, 0, s>>>(ix, desc, rot, hp);
   return cudaGetLastError();
 }
 

@@ -240,7 +240,7 @@ cudaError_t launch_typed(const PackedCall& c, const HeadParams& hp, cudaStream_t
                       static_cast<int32_t>(c.heads_kv), static_cast<int32_t>(c.heads / c.heads_kv),
                       static_cast<int32_t>(c.d_k), static_cast<int32_t>(c.d_v), c.flags};
   const PackedIndex ix{c.cu, c.slot, c.pos, c.rows, static_cast<int32_t>(c.seqs), static_cast<int32_t>(c.slots), kRun};
-  cudaError_t e = launch_packed_plan(ix, desc, s);
+  cudaError_t e = launch_packed_plan(ix, desc, PackedRotation{nullptr, nullptr, 0, false}, hp, s);
   if (e != cudaSuccess) return e;
   const unsigned u = static_cast<unsigned>(units), kv = static_cast<unsigned>(c.heads_kv);
   if (xpos) rotation_kernel<<<dim3(u, 8), kThreads, 0, s>>>(desc, rot, static_cast<int>(c.d_k / 2), hp);
@@ -254,7 +254,7 @@ cudaError_t launch_typed(const PackedCall& c, const HeadParams& hp, cudaStream_t
 
 }  // namespace
 
-size_t packed_workspace_bytes(int64_t rows, int64_t seqs, int64_t heads_kv, int64_t d_k, int64_t d_v) {
+size_t packed_simt_workspace_bytes(int64_t rows, int64_t seqs, int64_t heads_kv, int64_t d_k, int64_t d_v) {
   const int64_t units = packed_units(rows, seqs, kRun);
   return a256(sizeof(RunDesc) * units) + a256(sizeof(float2) * rows * (d_k / 2)) +
          sizeof(float) * static_cast<size_t>(units * heads_kv * d_k * d_v);

@@ -396,7 +396,12 @@ int retnet_chunkwise_kernel(retnet_dims_t dims, retnet_dtype_t in_dtype, uint32_
 retnet_status_t retnet_debug_wait_timeouts(unsigned int* count, int clear) {
   if (!count) return RETNET_ERR_NULL_PTR;
   if (cudaDeviceSynchronize() != cudaSuccess) return RETNET_ERR_CUDA;
-  return from_cuda(tc_wait_timeouts(count, clear != 0));
+  unsigned int packed = 0;
+  const retnet_status_t st = from_cuda(tc_wait_timeouts(count, clear != 0));
+  if (st != RETNET_OK) return st;
+  const retnet_status_t sp = from_cuda(packed_wait_timeouts(&packed, clear != 0));
+  *count += packed;
+  return sp;
 }
 
 retnet_status_t retnet_debug_set_wait_budget(long long cycles) {
@@ -413,7 +418,11 @@ retnet_status_t retnet_fp16_range_errors(unsigned int* count, int clear) {
   if (st != RETNET_OK) return st;
   const retnet_status_t sb = from_cuda(bwd_fp16_overflows(&bwd, clear != 0));
   *count += bwd;
-  return sb;
+  if (sb != RETNET_OK) return sb;
+  unsigned int packed = 0;
+  const retnet_status_t sp = from_cuda(packed_fp16_overflows(&packed, clear != 0));
+  *count += packed;
+  return sp;
 }
 
 retnet_status_t retnet_retention_step(const void* q, const void* k, const void* v, void* o, int64_t batch,
@@ -525,6 +534,11 @@ retnet_status_t retnet_msr_epilogue(const void* y, const void* g, void* out, int
 namespace {
 bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
+size_t packed_workspace_bytes(int64_t rows, int64_t seqs, int64_t heads_kv, int64_t d_k, int64_t d_v) {
+  return std::max(packed_simt_workspace_bytes(rows, seqs, heads_kv, d_k, d_v),
+                  packed_tc_workspace_bytes(rows, seqs, heads_kv, d_k, d_v));
+}
+
 // What the packed call and its single-token form check alike; seqs: entries of slots and pos.
 retnet_status_t check_packed(const retnet_packed_t& d, retnet_dtype_t dtype, uint32_t flags) {
   if (!valid_dtype(dtype)) return RETNET_ERR_BAD_DTYPE;
@@ -581,6 +595,7 @@ retnet_status_t retnet_retention_packed(const void* q, const void* k, const void
   if ((st = check_device()) != RETNET_OK) return st;
   c.ws = workspace;
   c.ws_bytes = workspace_bytes;
+  if (packed_tc_supported(c, hp)) return from_cuda(launch_packed_tc(c, hp, static_cast<cudaStream_t>(stream)));
   return from_cuda(launch_packed_simt(c, hp, static_cast<cudaStream_t>(stream)));
 }
 
