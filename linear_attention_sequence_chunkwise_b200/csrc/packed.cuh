@@ -33,12 +33,13 @@ struct PackedIndex {
 
 inline int64_t packed_units(int64_t rows, int64_t seqs, int64_t run) { return rows / run + seqs; }
 
-// The rotation of a token is base x offset (complex products): base[unit][i][j] turns pair j by the
-// angle of the run's token 16 i, offset[r][j] by that of r further tokens, so that a kernel needs no
-// sine or cosine of its own.  base: [units][run / 16][half], offset: [16][half]; nullptr: not written.
+// The rotation of a token is base x offset (complex products): base[unit][i] turns the pairs by the
+// angle of the run's token 16 i, offset[r] by that of r further tokens, so that a kernel needs no sine
+// or cosine of its own.  base: [units][run / 16][2 half] floats, offset: [17][2 half]; nullptr: not
+// written.  A row holds, for every four pairs, their cosines and then their sines.
 struct PackedRotation {
-  float2* base;
-  float2* offset;
+  float* base;
+  float* offset;
   int half;
   bool xpos;
 };

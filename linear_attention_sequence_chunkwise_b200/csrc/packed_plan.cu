@@ -6,83 +6,83 @@
 namespace retnet {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 512;
 
 __device__ unsigned int g_packed_errors = 0;
 
-__device__ __forceinline__ float2 turn(const PackedRotation& rot, int64_t p, int j, const HeadParams& hp) {
+// Rotation of pair j by position p, into its places in a row.
+__device__ __forceinline__ void turn(float* row, const PackedRotation& rot, int64_t p, int j, const HeadParams& hp) {
   float s = 0.f, c = 1.f;
   if (rot.xpos) position_sincos(p, hp.theta[j], &s, &c);
-  return make_float2(c, s);
+  row[j / 4 * 8 + j % 4] = c;
+  row[j / 4 * 8 + 4 + j % 4] = s;
 }
 
 // One CTA a unit.  The sequence of a unit is the last one whose first unit is not behind it.  A call
 // whose cu_seqlens is out of order or leaves the rows has no runs; a sequence is refused (no run)
 // when its slot is out of range or an earlier sequence with tokens has it, or its position is
-// negative; one with slot < 0 or no tokens has none either.
+// negative; one with slot < 0 or no tokens has none either.  Bound by the latency of its few
+// dependent steps: the arrays of up to kThreads sequences are fetched at once and the rest is done
+// from shared memory.
 __global__ void __launch_bounds__(kThreads) plan_kernel(PackedIndex ix, RunDesc* __restrict__ desc, PackedRotation rot,
                                                         HeadParams hp) {
+  __shared__ int32_t cu[kThreads + 1], slots[kThreads];
+  __shared__ int64_t poss[kThreads];
+  __shared__ int total;
   const int tid = threadIdx.x;
   const int64_t u = blockIdx.x;
-  int bad = 0, before = 0;
-  for (int s = tid; s < ix.seqs; s += kThreads) {
-    const int64_t a = ix.cu[s], b = ix.cu[s + 1];
-    bad |= a < 0 || b < a || b > ix.rows;
-    before += a / ix.run + s <= u;
-  }
-  __shared__ int total;
   if (tid == 0) total = 0;
-  bad = __syncthreads_or(bad);
-  before = __reduce_add_sync(0xffffffffu, before);
-  if (tid % 32 == 0) atomicAdd(&total, before);
+  int bad = 0, before = 0;
+  for (int s0 = 0; s0 < ix.seqs; s0 += kThreads) {
+    const int s = s0 + tid;
+    if (s < ix.seqs) {
+      const int64_t a = ix.cu[s], b = ix.cu[s + 1];
+      if (s0 == 0) {
+        cu[s] = static_cast<int32_t>(a);
+        if (s + 1 == ix.seqs || tid + 1 == kThreads) cu[s + 1] = static_cast<int32_t>(b);
+        slots[s] = ix.slots[s];
+        poss[s] = ix.pos ? ix.pos[s] : 0;
+      }
+      bad |= a < 0 || b < a || b > ix.rows;
+      before += a / ix.run + s <= u;
+    }
+  }
   __syncthreads();
-  RunDesc d{0, 0, 0, 0, 0, 0, 0};
-  if (bad) {
+  before = __reduce_add_sync(0xffffffffu, before);
+  if (tid % 32 == 0 && before) atomicAdd(&total, before);
+  bad = __syncthreads_or(bad);
+  if (rot.offset && u == 0)
+    for (int e = tid; e < 17 * rot.half; e += kThreads)
+      turn(rot.offset + e / rot.half * 2 * rot.half, rot, e / rot.half, e % rot.half, hp);
+  const int s = total - 1;  // -1: the first sequence starts behind this unit
+  if (bad || s < 0) {
     if (tid == 0) {
-      if (u == 0) atomicAdd(&g_packed_errors, 1u);
-      desc[u] = d;
+      if (bad && u == 0) atomicAdd(&g_packed_errors, 1u);
+      desc[u] = RunDesc{0, 0, 0, 0, 0, 0, 0};
     }
     return;
   }
-  const int s = total - 1;  // -1: the first sequence starts behind this unit
+  const bool cached = s < kThreads;
+  const int64_t a = cached ? cu[s] : ix.cu[s], len = (cached ? cu[s + 1] : ix.cu[s + 1]) - a;
+  const int32_t slot = cached ? slots[s] : ix.slots[s];
+  const int64_t pos = cached ? poss[s] : ix.pos ? ix.pos[s] : 0;
   int dup = 0;
-  if (s >= 0) {
-    const int32_t slot = ix.slots[s];
-    for (int j = tid; j < s; j += kThreads) dup |= ix.slots[j] == slot && ix.cu[j + 1] > ix.cu[j];
-  }
+  for (int j = tid; j < s; j += kThreads)
+    dup |= cached ? slots[j] == slot && cu[j + 1] > cu[j] : ix.slots[j] == slot && ix.cu[j + 1] > ix.cu[j];
   dup = __syncthreads_or(dup);
-  __shared__ int64_t first;  // the run's position, -1 without a run
-  if (tid == 0) first = -1;
-  if (rot.offset && u == 0) {
-    for (int e = tid; e < 16 * rot.half; e += kThreads) rot.offset[e] = turn(rot, e / rot.half, e % rot.half, hp);
+  const int64_t i = u - (a / ix.run + s), runs = (len + ix.run - 1) / ix.run, left = len - i * ix.run;
+  const bool wanted = i < runs && slot >= 0, refused = dup || slot >= ix.n_slots || pos < 0;
+  const bool live = wanted && !refused;
+  if (tid == 0) {
+    if (wanted && refused && i == 0) atomicAdd(&g_packed_errors, 1u);
+    desc[u] = live ? RunDesc{s, static_cast<int32_t>(a + i * ix.run), static_cast<int32_t>(left < ix.run ? left : ix.run),
+                             static_cast<int32_t>(i), static_cast<int32_t>(runs), slot, pos + i * ix.run}
+                   : RunDesc{0, 0, 0, 0, 0, 0, 0};
   }
-  if (tid == 0 && s >= 0) {
-    const int64_t a = ix.cu[s], len = ix.cu[s + 1] - a, pos = ix.pos ? ix.pos[s] : 0;
-    const int32_t slot = ix.slots[s];
-    const int64_t i = u - (a / ix.run + s), runs = (len + ix.run - 1) / ix.run;
-    if (i < runs && slot >= 0) {
-      if (dup || slot >= ix.n_slots || pos < 0) {
-        if (i == 0) atomicAdd(&g_packed_errors, 1u);
-      } else {
-        const int64_t left = len - i * ix.run;
-        d.seq = s;
-        d.row = static_cast<int32_t>(a + i * ix.run);
-        d.tokens = static_cast<int32_t>(left < ix.run ? left : ix.run);
-        d.index = static_cast<int32_t>(i);
-        d.runs = static_cast<int32_t>(runs);
-        d.slot = slot;
-        d.pos = pos + i * ix.run;
-        first = d.pos;
-      }
-    }
-  }
-  if (tid == 0) desc[u] = d;
-  if (!rot.base) return;
-  __syncthreads();
-  if (first < 0) return;
-  const int n = ix.run / 16 * rot.half;
-  for (int e = tid; e < n; e += kThreads)
-    rot.base[u * n + e] = turn(rot, first + 16 * (e / rot.half), e % rot.half, hp);
+  if (!rot.base || !live) return;
+  const int rows = ix.run / 16;
+  for (int e = tid; e < rows * rot.half; e += kThreads)
+    turn(rot.base + (u * rows + e / rot.half) * 2 * rot.half, rot, pos + i * ix.run + 16 * (e / rot.half), e % rot.half, hp);
 }
 
 }  // namespace

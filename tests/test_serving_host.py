@@ -19,7 +19,7 @@ def lib():
 
 
 def _fp(a):
-    return a.ctypes.data_as(rn._fp)
+    return rn._address(a)
 
 
 def _dims(**kw):
