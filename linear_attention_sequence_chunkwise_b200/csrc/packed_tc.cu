@@ -35,13 +35,21 @@ struct TcPackedArgs {
   const RunDesc* desc;
   const float* base;    // [units][8][d_k], rotations (packed.cuh)
   const float* offset;  // [17][d_k]
-  float* w;              // [units][heads_kv][d_k][d_v]
-  __half* r16;           // [units][heads_kv][d_k][d_v]
+  float* w;             // [units][heads_kv] states of chunks, in blocks of eight columns (below)
+  __half* r16;          // [units][heads_kv] states before the chunks, the same
   const int32_t* cu;
   int64_t units, stride_q, stride_k, stride_v, stride_o;
   int32_t kv, group, d_k, d_v;
   uint32_t flags;
+  bool o_wide;  // rows of o start on 32-byte boundaries
 };
+
+// States in the workspace are [d_v / 8][d_k][8]: a thread that holds a row of d_k writes eight columns
+// at once beside its neighbours' (a row-major state cost 32 separate lines a store), and 64 columns of
+// fp16 are the un-swizzled operand of the tensor cores as they lie.
+__device__ __forceinline__ int64_t blocked(int row, int col, int d_k) {
+  return (static_cast<int64_t>(col / 8) * d_k + row) * 8 + col % 8;
+}
 
 // Pairs of floats for the packed fp32 instructions (two lanes an instruction).
 using Two = uint64_t;
@@ -167,7 +175,6 @@ struct StateCfg {
   static constexpr int kPlane = kStep * M * 2, kVBytes = kStep * NV * 2;
   static constexpr int kSmem = 4 * kPlane + 2 * kVBytes + 1024;  // raw / first planes x 2, second, third, v x 2
   static constexpr int kCols = NV;
-  static_assert(M * NV * 4 <= 4 * kPlane + 2 * kVBytes, "the result is staged over the operands");
 };
 
 template <int M, int NV>
@@ -269,28 +276,24 @@ __global__ void __launch_bounds__(256, 2) tc_state_kernel(TcPackedArgs a, HeadPa
   dead = __syncthreads_or(dead);
   tc_fence_after();
   if (!dead) {
-    // Row i of d_k in lane i (M = 128), or in lane 32 (i / 16) + i % 16 (M = 64).  Staged in shared
-    // memory, 16-byte pieces swizzled by the row, so that global rows are written whole.
+    // row i of d_k in lane i (M = 128), or in lane 32 (i / 16) + i % 16 (M = 64)
     const int quarter = warp % 4;
-    const int row = M == 128 ? quarter * 32 + lane : quarter * 16 + lane;
+    const int row = k0 + (M == 128 ? quarter * 32 + lane : quarter * 16 + lane);
     const uint32_t lanes = tm + (static_cast<uint32_t>(quarter * 32) << 16);
+    float* w = a.w + (static_cast<int64_t>(blockIdx.x) * a.kv + h) * a.d_k * a.d_v;
 #pragma unroll
     for (int c = (warp / 4) * 32; c < NV; c += 64) {
       uint32_t r[2][16];
       tmem_ld_wait(lanes + c, r);
       if (M == 128 || lane < 16) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          st_shared_v4(sm + row * (NV * 4) + (((c / 4 + e) ^ (row & 7)) << 4), r[e / 4][(e % 4) * 4], r[e / 4][(e % 4) * 4 + 1],
-                       r[e / 4][(e % 4) * 4 + 2], r[e / 4][(e % 4) * 4 + 3]);
+        for (int e = 0; e < 32; e += 8) {
+          uint32_t x[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[j] = r[e / 16][e % 16 + j];
+          st_global_v8(w + blocked(row, v0 + c + e, a.d_k), x);
+        }
       }
-    }
-    __syncthreads();
-    float* w = a.w + (static_cast<int64_t>(blockIdx.x) * a.kv + h) * a.d_k * a.d_v + v0;
-    for (int e = tid; e < M * NV / 4; e += 256) {
-      const int i = e / (NV / 4), c = e % (NV / 4);
-      *reinterpret_cast<uint4*>(w + static_cast<int64_t>(k0 + i) * a.d_v + c * 4) =
-          ld_shared_u4(sm + i * (NV * 4) + ((c ^ (i & 7)) << 4));
     }
   }
   tc_fence_before();
@@ -303,13 +306,16 @@ __global__ void __launch_bounds__(256, 2) tc_state_kernel(TcPackedArgs a, HeadPa
 
 // ---- state of whole sequences ----------------------------------------------------------------
 // CTA = (sequence, key/value head, up to 128 rows of d_k x NV columns of d_v): the chunks in order, the
-// fp32 state in registers (at most 64 values a thread); before each chunk its fp16 rounding goes to r16, after
-// the last the state goes to the pool.  No W, no scan.  Steps of 64 tokens run through a ring: copies
-// two steps ahead, k of the next step is cut while the products of this one run.
+// fp32 state in registers (at most 64 values a thread); before each chunk its fp16 rounding goes to
+// r16, after the last the state goes to the pool.  No W, no scan.  Steps of 64 tokens run through a
+// ring: copies two steps ahead; the data warps cut k of the next step, and add and round the last
+// chunk's state, while a warp of its own issues this step's products (a data warp that issued them
+// held the others up for as long as they ran).
 template <int M, int NV>
 struct SeqCfg {
-  static constexpr int kThreads = NV == 256 ? 512 : 256;
-  static constexpr int kHold = NV * 128 / kThreads;  // state values a thread
+  static constexpr int kData = NV == 256 ? 512 : 256;
+  static constexpr int kThreads = kData + 32;
+  static constexpr int kHold = NV * 128 / kData;  // state values a thread
   static constexpr int kStep = 64;
   static constexpr int kPlane = kStep * M * 2, kVBytes = kStep * NV * 2;
   static constexpr int kSmem = 3 * kPlane + 4 * kPlane + 3 * kVBytes + 1024;
@@ -320,7 +326,7 @@ template <int M, int NV>
 __global__ void __launch_bounds__(SeqCfg<M, NV>::kThreads, 1) tc_sequence_kernel(TcPackedArgs a, HeadParams hp) {
   using C = SeqCfg<M, NV>;
   extern __shared__ unsigned char raw_smem[];
-  __shared__ uint64_t bars[2];
+  __shared__ uint64_t bars[4];  // products of even / odd steps done; operands of even / odd steps ready
   __shared__ uint32_t tmem_at;
   pdl_go();
   pdl_wait();
@@ -333,147 +339,160 @@ __global__ void __launch_bounds__(SeqCfg<M, NV>::kThreads, 1) tc_sequence_kernel
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int k0 = (blockIdx.z / slices) * M, v0 = (blockIdx.z % slices) * NV;
   const uint32_t sm = (smem_addr(raw_smem) + 1023u) & ~1023u, s2 = sm + 3 * C::kPlane, sv = s2 + 4 * C::kPlane;
-  const uint32_t b0 = smem_addr(&bars[0]), b1 = smem_addr(&bars[1]);
-  constexpr int kGroups = M / 8, kRows = C::kThreads / kGroups, kPer = C::kStep / kRows;
-  static_assert(kRows % 16 == 0, "a thread's rows share their place in a group of 16 tokens");
-  const int g = tid % kGroups, tr = tid / kGroups;
-  const __nv_bfloat16* kp = a.k + static_cast<int64_t>(d.row) * a.stride_k + static_cast<int64_t>(h) * a.d_k + k0 + g * 8;
-  const __nv_bfloat16* vp = a.v + static_cast<int64_t>(d.row) * a.stride_v + static_cast<int64_t>(h) * a.d_v + v0;
-  const uint32_t mine = (g / 8) * (C::kStep * 128);
-  auto fetch = [&](int st) {
-    if (st < steps) {
-      const int slot = st % 3;
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int r = tr + i * kRows, t = st * C::kStep + r;
-        const bool in = t < len;
-        cp_async16(sm + slot * C::kPlane + mine + sw128(r, g % 8), kp + static_cast<int64_t>(in ? t : 0) * a.stride_k, in);
-      }
-#pragma unroll
-      for (int i = 0; i < C::kStep * (NV / 8) / C::kThreads; ++i) {
-        const int e = tid + i * C::kThreads, r = e / (NV / 8), c = e % (NV / 8), t = st * C::kStep + r;
-        const bool in = t < len;
-        cp_async16(sv + slot * C::kVBytes + (c / 8) * (C::kStep * 128) + sw128(r, c % 8),
-                   vp + static_cast<int64_t>(in ? t : 0) * a.stride_v + c * 8, in);
-      }
-    }
-    cp_async_commit();
-  };
-  fetch(0);
-  fetch(1);
+  const uint32_t done = smem_addr(&bars[0]), ready = smem_addr(&bars[2]);
   if (warp == 0) {
     tmem_alloc(smem_addr(&tmem_at), C::kCols);
     tmem_relinquish();
   }
   if (tid == 0) {
-    mbar_init(b0, 1);
-    mbar_init(b1, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(done + 8 * i, 1);
+      mbar_init(ready + 8 * i, C::kData / 32);
+    }
     fence_mbar_init();
   }
-  const float lg = hp.log2g[h];
-  const Turn off = scaled(load_turn(a.offset + (tr % 16) * a.d_k + k0 + g * 8), decay_pow(lg, 15 - tr % 16));
-  const float* base = a.base + u0 * 8 * a.d_k + k0 + g * 8;
-  // this thread's piece of the state: row (k0 + row), columns v0 + cols on
-  const int quarter = warp % 4, cols = (warp / 4) * C::kHold;
-  const bool holds = M == 128 || lane < 16;
-  const int row = k0 + (M == 128 ? quarter * 32 + lane : quarter * 16 + lane % 16);
-  const int64_t at_state = static_cast<int64_t>(h) * a.d_k * a.d_v + static_cast<int64_t>(row) * a.d_v + v0 + cols;
-  const int64_t state_size = static_cast<int64_t>(a.kv) * a.d_k * a.d_v;
-  float* pool = a.pool + d.slot * state_size + at_state;
-  __half* r16 = a.r16 + u0 * state_size + at_state;
-  float S[C::kHold];
-#pragma unroll
-  for (int e = 0; e < C::kHold; e += 4) {
-    const float4 x = d.pos > 0 && holds ? *reinterpret_cast<const float4*>(pool + e) : make_float4(0.f, 0.f, 0.f, 0.f);
-    S[e] = x.x; S[e + 1] = x.y; S[e + 2] = x.z; S[e + 3] = x.w;
-  }
-  __half2 mx = __float2half2_rn(0.f);
-  auto emit = [&](int chunk) {
-#pragma unroll
-    for (int e = 0; e < C::kHold; e += 16) {
-      uint32_t w[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        w[j] = pack_f16x2(S[e + 2 * j], S[e + 2 * j + 1]);
-        track(mx, w[j]);
-      }
-      if (holds) st_global_v8(r16 + chunk * state_size + e, w);
-    }
-  };
-  if (d.pos > 0) emit(0);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tm = tmem_at;
-  // S <- S + less S + up D, D the products of a chunk
-  auto add_chunk = [&](int chunk, float less, float up) {
+  auto slot_of = [&](int st) { return st % 3; };
+  auto products_done = [&](int st) { return mbar_wait(done + 8 * (st & 1), (st >> 1) & 1, kDrainBudget); };
+
+  if (warp == C::kData / 32) {
+    if (lane == 0) {
+      constexpr uint32_t ID = idesc_bf16_f32(M, NV, 1, 1);
+      int st = 0;
+      for (; st < steps; ++st) {
+        if (!mbar_wait(ready + 8 * (st & 1), (st >> 1) & 1, kDrainBudget)) break;
+        tc_fence_after();
+        const uint64_t dv = sdesc_sw128(sv + slot_of(st) * C::kVBytes, C::kStep * 128, 1024);
+        const uint64_t d0 = sdesc_sw128(sm + slot_of(st) * C::kPlane, C::kStep * 128, 1024);
+        const uint64_t d1 = sdesc_sw128(s2 + (st & 1) * 2 * C::kPlane, C::kStep * 128, 1024);
+        const uint32_t tD = tm + ((st >> 1) & 1) * NV;
 #pragma unroll
-    for (int e = 0; e < C::kHold; e += 32) {
-      uint32_t r[2][16];
-      tmem_ld_wait(tm + (static_cast<uint32_t>(quarter * 32) << 16) + (chunk & 1) * NV + cols + e, r);
+        for (int p = 2; p >= 0; --p) {  // the small planes first
+          const uint64_t dk = p == 0 ? d0 : d1 + (((p - 1) * C::kPlane) >> 4);
 #pragma unroll
-      for (int j = 0; j < 32; ++j)
-        S[e + j] = fmaf(less, S[e + j], fmaf(up, __uint_as_float(r[j / 16][j % 16]), S[e + j]));
-    }
-    tc_fence_before();
-  };
-  constexpr uint32_t ID = idesc_bf16_f32(M, NV, 1, 1);
-  const float full_less = decay_less_one(lg, kChunk);
-  bool dead = false;
-  auto wait_step = [&](int st) { dead |= !mbar_wait(st & 1 ? b1 : b0, (st >> 1) & 1, kDrainBudget); };
-  for (int st = 0; st < steps; ++st) {
-    cp_async_wait<1>();
-    const uint32_t hi = sm + (st % 3) * C::kPlane, low = s2 + (st & 1) * 2 * C::kPlane;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int r = tr + i * kRows, at = st * (C::kStep / 16) + r / 16;  // base rows of a chunk are 8, in order
-      const uint32_t to = mine + sw128(r, g % 8);
-      Eight y = turned(ld_shared_u4(hi + to), product(scaled(load_turn(base + static_cast<int64_t>(at) * a.d_k),
-                                                             decay_pow(lg, 112 - 16 * (at % 8))), off));
-      store_plane(hi + to, y);
-      store_plane(low + to, y);
-      store_plane(low + C::kPlane + to, y);
-    }
-    fence_proxy_async_smem();
-    if (__syncthreads_or(dead)) {
-      dead = true;
-      break;
-    }
-    tc_fence_after();
-    if (tid == 0) {
-      const uint64_t dv = sdesc_sw128(sv + (st % 3) * C::kVBytes, C::kStep * 128, 1024);
-      const uint32_t tD = tm + ((st >> 1) & 1) * NV;
-#pragma unroll
-      for (int p = 2; p >= 0; --p) {
-        const uint64_t dk = sdesc_sw128(p == 0 ? hi : low + (p - 1) * C::kPlane, C::kStep * 128, 1024);
-#pragma unroll
-        for (int ks = 0; ks < C::kStep / 16; ++ks)
-          mma_f16_ss(tD, dk + ((ks * 2048) >> 4), dv + ((ks * 2048) >> 4), ID, st % 2 || p < 2 || ks > 0);
+          for (int ks = 0; ks < C::kStep / 16; ++ks)
+            mma_f16_ss(tD, dk + ((ks * 2048) >> 4), dv + ((ks * 2048) >> 4), ID, st % 2 || p < 2 || ks > 0);
+        }
+        mma_commit(done + 8 * (st & 1));
       }
-      mma_commit(st & 1 ? b1 : b0);
+      if (st > 0) products_done(st - 1);
     }
-    if (st > 0) wait_step(st - 1);  // its ring slot is free
-    fetch(st + 2);
-    if (st > 0 && st % 2 == 0) {  // the chunk before this step is complete; the next one's products run
-      tc_fence_after();
-      add_chunk(st / 2 - 1, full_less, 1.f);
-      emit(st / 2);
-    }
-  }
-  if (!dead) wait_step(steps - 1);
-  dead = __syncthreads_or(dead);
-  if (!dead) {
-    tc_fence_after();
-    const int last = len - (d.runs - 1) * kChunk;
-    add_chunk(d.runs - 1, decay_less_one(lg, last), exp2f(static_cast<float>(last - kChunk) * lg));
-    if (holds) {
+  } else {
+    constexpr int kGroups = M / 8, kRows = C::kData / kGroups, kPer = C::kStep / kRows;
+    static_assert(kRows % 16 == 0, "a thread's rows share their place in a group of 16 tokens");
+    const int g = tid % kGroups, tr = tid / kGroups;
+    const __nv_bfloat16* kp = a.k + static_cast<int64_t>(d.row) * a.stride_k + static_cast<int64_t>(h) * a.d_k + k0 + g * 8;
+    const __nv_bfloat16* vp = a.v + static_cast<int64_t>(d.row) * a.stride_v + static_cast<int64_t>(h) * a.d_v + v0;
+    const uint32_t mine = (g / 8) * (C::kStep * 128) + sw128(tr, g % 8);  // kRows more rows: kRows * 128 bytes on
+    constexpr int kVPer = C::kStep * (NV / 8) / C::kData, kVRows = C::kData / (NV / 8);
+    const int vr = tid / (NV / 8), vc = tid % (NV / 8);
+    static_assert(kVRows % 8 == 0, "rows kVRows apart are swizzled alike");
+    const uint32_t v_mine = (vc / 8) * (C::kStep * 128) + sw128(vr, vc % 8);
+    auto fetch = [&](int st) {
+      if (st < steps) {
+        const uint32_t tk = sm + slot_of(st) * C::kPlane + mine, tv = sv + slot_of(st) * C::kVBytes + v_mine;
 #pragma unroll
-      for (int e = 0; e < C::kHold; e += 4)
-        *reinterpret_cast<float4*>(pool + e) = make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);
+        for (int i = 0; i < kPer; ++i) {
+          const int t = st * C::kStep + tr + i * kRows;
+          const bool in = t < len;
+          cp_async16(tk + i * kRows * 128, kp + static_cast<int64_t>(in ? t : 0) * a.stride_k, in);
+        }
+#pragma unroll
+        for (int i = 0; i < kVPer; ++i) {
+          const int t = st * C::kStep + vr + i * kVRows;
+          const bool in = t < len;
+          cp_async16(tv + i * kVRows * 128, vp + static_cast<int64_t>(in ? t : 0) * a.stride_v + vc * 8, in);
+        }
+      }
+      cp_async_commit();
+    };
+    fetch(0);
+    fetch(1);
+    const float lg = hp.log2g[h];
+    const Turn off = scaled(load_turn(a.offset + (tr % 16) * a.d_k + k0 + g * 8), decay_pow(lg, 15 - tr % 16));
+    const float* base = a.base + u0 * 8 * a.d_k + k0 + g * 8;
+    // this thread's piece of the state: row (k0 + row), columns v0 + cols on
+    const int quarter = warp % 4, cols = v0 + (warp / 4) * C::kHold;
+    const bool holds = M == 128 || lane < 16;
+    const int row = k0 + (M == 128 ? quarter * 32 + lane : quarter * 16 + lane % 16);
+    const int64_t state_size = static_cast<int64_t>(a.kv) * a.d_k * a.d_v, at_head = static_cast<int64_t>(h) * a.d_k * a.d_v;
+    float* pool = a.pool + d.slot * state_size + at_head + static_cast<int64_t>(row) * a.d_v + cols;
+    __half* r16 = a.r16 + u0 * state_size + at_head + blocked(row, cols, a.d_k);
+    float S[C::kHold];
+#pragma unroll
+    for (int e = 0; e < C::kHold; e += 4) {
+      const float4 x = d.pos > 0 && holds ? *reinterpret_cast<const float4*>(pool + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+      S[e] = x.x; S[e + 1] = x.y; S[e + 2] = x.z; S[e + 3] = x.w;
     }
+    __half2 mx = __float2half2_rn(0.f);
+    auto emit = [&](int chunk) {
+      __half* to = r16 + chunk * state_size;
+#pragma unroll
+      for (int e = 0; e < C::kHold; e += 8) {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          w[j] = pack_f16x2(S[e + 2 * j], S[e + 2 * j + 1]);
+          track(mx, w[j]);
+        }
+        if (holds) *reinterpret_cast<uint4*>(to + static_cast<int64_t>(e) * a.d_k) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    };
+    if (d.pos > 0) emit(0);
+    // S <- S + less S + up D, D the products of a chunk
+    auto add_chunk = [&](int chunk, float less, float up) {
+#pragma unroll
+      for (int e = 0; e < C::kHold; e += 32) {
+        uint32_t r[2][16];
+        tmem_ld_wait(tm + (static_cast<uint32_t>(quarter * 32) << 16) + (chunk & 1) * NV + (warp / 4) * C::kHold + e, r);
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          S[e + j] = fmaf(less, S[e + j], fmaf(up, __uint_as_float(r[j / 16][j % 16]), S[e + j]));
+      }
+      tc_fence_before();
+    };
+    const float full_less = decay_less_one(lg, kChunk);
+    bool alive = true;
+    for (int st = 0; st < steps; ++st) {
+      cp_async_wait<1>();
+      const uint32_t hi = sm + slot_of(st) * C::kPlane + mine, low = s2 + (st & 1) * 2 * C::kPlane + mine;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int at = st * (C::kStep / 16) + (tr + i * kRows) / 16;  // base rows of a chunk are 8, in order
+        const uint32_t o = i * kRows * 128;
+        Eight y = turned(ld_shared_u4(hi + o), product(scaled(load_turn(base + static_cast<int64_t>(at) * a.d_k),
+                                                              decay_pow(lg, 112 - 16 * (at % 8))), off));
+        store_plane(hi + o, y);
+        store_plane(low + o, y);
+        store_plane(low + C::kPlane + o, y);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ready + 8 * (st & 1));
+      if (st > 0 && !(alive = products_done(st - 1))) break;  // its ring slot and small planes are free
+      fetch(st + 2);
+      if (st > 0 && st % 2 == 0) {  // the chunk before this step is complete
+        tc_fence_after();
+        add_chunk(st / 2 - 1, full_less, 1.f);
+        emit(st / 2);
+      }
+    }
+    if (alive && products_done(steps - 1)) {
+      tc_fence_after();
+      const int last = len - (d.runs - 1) * kChunk;
+      add_chunk(d.runs - 1, decay_less_one(lg, last), exp2f(static_cast<float>(last - kChunk) * lg));
+      if (holds) {
+#pragma unroll
+        for (int e = 0; e < C::kHold; e += 4)
+          *reinterpret_cast<float4*>(pool + e) = make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);
+      }
+    }
+    report(mx);
+    cp_async_wait<0>();
   }
-  report(mx);
-  cp_async_wait<0>();
   tc_fence_before();
   __syncthreads();
   if (warp == 0) {
@@ -483,7 +502,7 @@ __global__ void __launch_bounds__(SeqCfg<M, NV>::kThreads, 1) tc_sequence_kernel
 }
 
 // ---- scan ------------------------------------------------------------------------------------
-// Thread = four columns of one (sequence, head) state.  The decay after a chunk is gamma^128 except
+// Thread = four columns of one (sequence, head) state, in the order of the blocked states.  The decay after a chunk is gamma^128 except
 // the last's; a short last chunk's W is relative to token 127, so it is scaled back by
 // gamma^(len-128) <= 2^12.
 constexpr int kScanThreads = 256;
@@ -497,7 +516,9 @@ __global__ void __launch_bounds__(kScanThreads) tc_scan_kernel(TcPackedArgs a, H
   if (u0 < 0 || u0 >= a.units) return;  // cu_seqlens out of order: no run has tokens
   const RunDesc first = a.desc[u0];
   if (first.tokens == 0 || first.seq != s || e >= n4) return;
-  float4* slot = reinterpret_cast<float4*>(a.pool) + (static_cast<int64_t>(first.slot) * a.kv + h) * n4 + e;
+  const int block = static_cast<int>(e / (2 * a.d_k)), in = static_cast<int>(e % (2 * a.d_k));  // (column block, half row)
+  float4* slot = reinterpret_cast<float4*>(a.pool + (static_cast<int64_t>(first.slot) * a.kv + h) * 4 * n4 +
+                                           static_cast<int64_t>(in / 2) * a.d_v + block * 8 + in % 2 * 4);
   float4 r = first.pos > 0 ? *slot : make_float4(0.f, 0.f, 0.f, 0.f);
   const float lg = hp.log2g[h], full_less = decay_less_one(lg, kChunk);
   const int64_t step = static_cast<int64_t>(a.kv) * n4;
@@ -537,22 +558,28 @@ __global__ void __launch_bounds__(kScanThreads) tc_scan_kernel(TcPackedArgs a, H
 }
 
 // ---- output ----------------------------------------------------------------------------------
-// CTA = (chunk, query head).  q and k arrive by asynchronous copies and are rotated and rounded in
-// place; the scores are computed once and kept in tensor memory as bf16 pairs.  Then, for every 64
-// columns of d_v, Q R + P V into one of two accumulators: R and V come through a ring whose last
-// stage lies over k (free after the scores), and a slice's epilogue (row factors, store) runs under
-// the next one's products.
+// CTA = (chunk, query head).  The data warps fetch q and k by asynchronous copies, rotate and round
+// them in place, turn the scores into bf16 pairs in tensor memory, and store the outputs: slice s
+// (64 columns of d_v) is the work of four of them, the others' slices run beside it.  One warp issues
+// all products (Q R + P V of a slice into the accumulator of its four warps), one fetches R (a bulk
+// copy: the workspace holds it as the tensor cores take it) and V through a ring whose last stage lies
+// over k, free after the scores.  When the data warps did all of this in turn, a slice cost 4800 cycles
+// (products 1800, copies 570, stores 1100, the rest barriers) at d_k 256.
 template <int DK>
 struct OutCfg {
-  static constexpr int kThreads = DK == 256 ? 512 : 256;
-  static constexpr int NV = 64;
+  static constexpr int kData = DK == 256 ? 512 : 256;
+  static constexpr int kThreads = kData + 64;
+  static constexpr int NV = 64, kTeams = kData / 128;
   static constexpr int kQ = kChunk * DK * 2;
   static constexpr int kR = DK * NV * 2, kV = kChunk * NV * 2, kStage = kR + kV;
   static constexpr int kOwn = DK == 128 ? 1 : 2;                 // ring stages besides k's area
   static constexpr int kRing = kOwn + (kQ >= kStage ? 1 : 0);
   static constexpr int kSmem = 2 * kQ + kOwn * kStage + 1024;
   static constexpr int kCtas = kSmem <= 110 * 1024 ? 2 : 1;
-  static constexpr int kCols = 256;  // S / P: 0..127, O: 128.. and 192..
+  static constexpr int kCols = 128 + kTeams * NV <= 256 ? 256 : 512;  // S / P: 0..127, then the accumulators
+  // A slice is fetched again only when the one kRing before it is done, and its accumulator's next
+  // products wait for that fetch: no barrier runs two phases ahead of one who waits.
+  static_assert(kRing <= kTeams, "phases");
 };
 
 template <int DK>
@@ -560,7 +587,8 @@ __global__ void __launch_bounds__(OutCfg<DK>::kThreads, OutCfg<DK>::kCtas) tc_ou
   using C = OutCfg<DK>;
   constexpr int NV = C::NV;
   extern __shared__ unsigned char raw_smem[];
-  __shared__ uint64_t bars[3];
+  // q and k ready; scores done; P ready; per ring stage: filled; per team: products done, read
+  __shared__ uint64_t bars[3 + C::kRing + 2 * C::kTeams];
   __shared__ uint32_t tmem_at;
   __shared__ float factor[kChunk];
   pdl_wait();
@@ -569,122 +597,178 @@ __global__ void __launch_bounds__(OutCfg<DK>::kThreads, OutCfg<DK>::kCtas) tc_ou
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int hq = blockIdx.y, h = hq / a.group, slices = a.d_v / NV;
   const uint32_t sq = (smem_addr(raw_smem) + 1023u) & ~1023u, sk = sq + C::kQ, own = sk + C::kQ;
-  const uint32_t bs = smem_addr(&bars[0]), bo[2] = {smem_addr(&bars[1]), smem_addr(&bars[2])};
-  constexpr int kGroups = DK / 8, kRows = C::kThreads / kGroups, kPer = kChunk / kRows;
-  static_assert(kRows % 16 == 0, "a thread's rows share their place in a group of 16 tokens");
-  const int g = tid % kGroups, tr = tid / kGroups;
-  const float lg = hp.log2g[h];
-  const __nv_bfloat16* qp = a.q + static_cast<int64_t>(d.row) * a.stride_q + static_cast<int64_t>(hq) * DK + g * 8;
-  const __nv_bfloat16* kp = a.k + static_cast<int64_t>(d.row) * a.stride_k + static_cast<int64_t>(h) * DK + g * 8;
-  const __nv_bfloat16* vp = a.v + static_cast<int64_t>(d.row) * a.stride_v + static_cast<int64_t>(h) * a.d_v;
-  const __half* rp = a.r16 + (static_cast<int64_t>(blockIdx.x) * a.kv + h) * DK * a.d_v;
+  const uint32_t b_qk = smem_addr(bars), b_s = b_qk + 8, b_p = b_qk + 16, b_full = b_qk + 24, b_done = b_full + 8 * C::kRing,
+                 b_read = b_done + 8 * C::kTeams;
   const bool has_r = !(d.index == 0 && d.pos == 0);
-  const uint32_t mine = (g / 8) * kBlock;
-  auto fetch_rows = [&](uint32_t to, const __nv_bfloat16* p, int64_t stride) {
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int t = tr + i * kRows;
-      const bool in = t < d.tokens;
-      cp_async16(to + mine + sw128(t, g % 8), p + static_cast<int64_t>(in ? t : 0) * stride, in);
-    }
-    cp_async_commit();
-  };
   auto stage = [&](int s) -> uint32_t {
     const int i = s % C::kRing;
     return i < C::kOwn ? own + i * C::kStage : sk;
   };
-  auto fetch_slice = [&](int s) {
-    if (s < slices) {
-      const uint32_t to = stage(s), tv = to + C::kR;
-      const int v0 = s * NV;
-      if (has_r) {
-#pragma unroll
-        for (int i = 0; i < DK * (NV / 8) / C::kThreads; ++i) {
-          const int e = tid + i * C::kThreads, r = e / (NV / 8), c = e % (NV / 8);
-          cp_async16(to + sw128(r, c), rp + static_cast<int64_t>(r) * a.d_v + v0 + c * 8, true);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < kChunk * (NV / 8) / C::kThreads; ++i) {
-        const int e = tid + i * C::kThreads, r = e / (NV / 8), c = e % (NV / 8);
-        const bool in = r < d.tokens;
-        cp_async16(tv + sw128(r, c), vp + static_cast<int64_t>(in ? r : 0) * a.stride_v + v0 + c * 8, in);
-      }
-    }
-    cp_async_commit();
-  };
-  fetch_rows(sq, qp, a.stride_q);
-  fetch_rows(sk, kp, a.stride_k);
-#pragma unroll
-  for (int s = 0; s < C::kOwn; ++s) fetch_slice(s);
+  auto wait = [](uint32_t bar, int phase) { return mbar_wait(bar, phase & 1, kDrainBudget); };
+  auto done = [&](int s) { return wait(b_done + 8 * (s % C::kTeams), s / C::kTeams); };
   if (warp == 0) {
     tmem_alloc(smem_addr(&tmem_at), C::kCols);
     tmem_relinquish();
   }
-  if (tid == 0) {
-    mbar_init(bs, 1);
-    mbar_init(bo[0], 1);
-    mbar_init(bo[1], 1);
+  if (tid == C::kData) {
+    mbar_init(b_qk, C::kData / 32);
+    mbar_init(b_s, 1);
+    mbar_init(b_p, C::kData / 32);
+    for (int i = 0; i < C::kRing; ++i) mbar_init(b_full + 8 * i, 2);
+    for (int i = 0; i < C::kTeams; ++i) {
+      mbar_init(b_done + 8 * i, 1);
+      mbar_init(b_read + 8 * i, 4);
+    }
     fence_mbar_init();
   }
-  // rows t = tr + kRows i: each one's rotation is the last one's times a constant step
-  const Turn first = product(load_turn(a.base + (static_cast<int64_t>(blockIdx.x) * 8 + tr / 16) * DK + g * 8),
-                             load_turn(a.offset + (tr % 16) * DK + g * 8));
-  Turn step = load_turn(a.offset + 16 * DK + g * 8);
-  if (kRows == 32) step = product(step, step);
-  for (int i = tid; i < kChunk; i += C::kThreads) factor[i] = row_factor32(hp.gamma[h], DK, d.pos + i, a.flags);
-  __half2 mx = __float2half2_rn(0.f);
-  // q by gamma^(t+1), k by gamma^(127-t)
-  auto convert = [&](uint32_t area, float scale, float grow) {
-    Turn t = scaled(first, scale);
-    const Turn s = scaled(step, grow);
+
+  constexpr int kGroups = DK / 8, kRows = C::kData / kGroups, kPer = kChunk / kRows;
+  static_assert(kRows % 16 == 0, "a thread's rows share their place in a group of 16 tokens");
+  const int g = tid % kGroups, tr = tid / kGroups;
+  const uint32_t mine = (g / 8) * kBlock + sw128(tr, g % 8);  // kRows more rows: kRows * 128 bytes on
+  if (tid < C::kData) {
+    auto fetch_rows = [&](uint32_t to, const __nv_bfloat16* p, int64_t stride) {
+      const __nv_bfloat16* q = p + static_cast<int64_t>(tr) * stride;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const uint32_t to = area + mine + sw128(tr + i * kRows, g % 8);
-      const Eight y = turned(ld_shared_u4(to), t);
-      uint32_t w[4];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float2 u = parts(y.first[e]), v = parts(y.second[e]);
-        w[2 * e] = pack_f16x2(u.x, v.x);
-        w[2 * e + 1] = pack_f16x2(u.y, v.y);
-        track(mx, w[2 * e]);
-        track(mx, w[2 * e + 1]);
+      for (int i = 0; i < kPer; ++i, q += kRows * stride) {
+        const bool in = tr + i * kRows < d.tokens;
+        cp_async16(to + mine + i * kRows * 128, in ? q : p, in);
       }
-      st_shared_v4(to, w[0], w[1], w[2], w[3]);
-      if (i + 1 < kPer) t = product(t, s);
-    }
-  };
-  cp_async_wait<C::kOwn + 1>();
-  convert(sq, decay_pow(lg, tr + 1), decay_pow(lg, kRows));
-  cp_async_wait<C::kOwn>();
-  convert(sk, decay_pow(lg, kChunk - 1 - tr), exp2f(-static_cast<float>(kRows) * lg));
-  report(mx);
-  fence_proxy_async_smem();
+      cp_async_commit();
+    };
+    fetch_rows(sq, a.q + static_cast<int64_t>(d.row) * a.stride_q + static_cast<int64_t>(hq) * DK + g * 8, a.stride_q);
+    fetch_rows(sk, a.k + static_cast<int64_t>(d.row) * a.stride_k + static_cast<int64_t>(h) * DK + g * 8, a.stride_k);
+  } else {
+    for (int i = tid - C::kData; i < kChunk; i += 64) factor[i] = row_factor32(hp.gamma[h], DK, d.pos + i, a.flags);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tm = tmem_at, tS = tm;
-  // descriptors once, then constants added: built anew for every product they were most of a slice's time
-  const uint64_t dq = sdesc_sw128(sq, 16, 1024);
-  auto kstep = [](int ks) -> uint64_t { return static_cast<uint64_t>(((ks / 4) * kBlock + (ks % 4) * 32) >> 4); };
-  if (tid == 0) {
-    constexpr uint32_t ID = idesc_f16_f32(kChunk, kChunk, 0, 0);
-    const uint64_t dk = sdesc_sw128(sk, 16, 1024);
+
+  if (warp == C::kData / 32) {  // ---- products
+    if (lane == 0) {
+      // descriptors once, then constants added
+      const uint64_t dq = sdesc_sw128(sq, 16, 1024), dk = sdesc_sw128(sk, 16, 1024);
+      auto kstep = [](int ks) -> uint64_t { return static_cast<uint64_t>(((ks / 4) * kBlock + (ks % 4) * 32) >> 4); };
+      bool ok = wait(b_qk, 0);
+      if (ok) {
+        tc_fence_after();
+        constexpr uint32_t ID = idesc_f16_f32(kChunk, kChunk, 0, 0);
 #pragma unroll
-    for (int ks = 0; ks < DK / 16; ++ks) mma_f16_ss(tS, dq + kstep(ks), dk + kstep(ks), ID, ks > 0);
-    mma_commit(bs);
-  }
-  bool dead = !mbar_wait(bs, 0, kDrainBudget);
-  if (!__syncthreads_or(dead)) {
-    tc_fence_after();
-    if (C::kRing > C::kOwn) fetch_slice(C::kOwn);
-    const int quarter = warp % 4, row = quarter * 32 + lane;
+        for (int ks = 0; ks < DK / 16; ++ks) mma_f16_ss(tS, dq + kstep(ks), dk + kstep(ks), ID, ks > 0);
+        mma_commit(b_s);
+        ok = wait(b_p, 0);
+      }
+      int s = 0;
+      for (; ok && s < slices; ++s) {
+        const int team = s % C::kTeams;
+        ok = wait(b_full + 8 * (s % C::kRing), s / C::kRing) && (s < C::kTeams || wait(b_read + 8 * team, s / C::kTeams - 1));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t tO = tm + 128 + team * NV, at = stage(s);
+        const uint64_t dr = sdesc_cores(at, DK * 16, 128), dv = sdesc_sw128(at + C::kR, kBlock, 1024);
+        if (has_r) {
+          constexpr uint32_t ID = idesc_f16_f32(kChunk, NV, 0, 1);
+#pragma unroll
+          for (int ks = 0; ks < DK / 16; ++ks) mma_f16_ss(tO, dq + kstep(ks), dr + ((ks * 256) >> 4), ID, ks > 0);
+        }
+        constexpr uint32_t ID = idesc_bf16_f32(kChunk, NV, 0, 1);
+#pragma unroll
+        for (int part = 1; part >= 0; --part)
+#pragma unroll
+          for (int ks = 0; ks < kChunk / 16; ++ks)
+            mma_f16_ts(tO, tS + (ks / 2) * 32 + part * 16 + (ks % 2) * 8, dv + ((ks * 2048) >> 4), ID,
+                       has_r || part == 0 || ks > 0);
+        mma_commit(b_done + 8 * team);
+      }
+      wait(b_s, 0);
+      if (s > 0) done(s - 1);  // nothing in flight when the tensor memory is freed
+    }
+  } else if (warp == C::kData / 32 + 1) {  // ---- R and V
+    const __nv_bfloat16* vp = a.v + static_cast<int64_t>(d.row) * a.stride_v + static_cast<int64_t>(h) * a.d_v +
+                              static_cast<int64_t>(lane / 8) * a.stride_v + lane % 8 * 8;
+    const __half* rp = a.r16 + (static_cast<int64_t>(blockIdx.x) * a.kv + h) * DK * a.d_v;
+    auto filled = [&](int s) {  // this warp's copies of slice s have landed
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(b_full + 8 * (s % C::kRing));
+    };
+    bool ok = true;
+    int s = 0;
+    for (; s < slices; ++s) {
+      if (s >= C::kRing) ok = done(s - C::kRing);
+      else if (s >= C::kOwn) ok = wait(b_s, 0);
+      if (!ok) break;
+      const uint32_t to = stage(s), bar = b_full + 8 * (s % C::kRing);
+      if (lane == 0) {
+        if (has_r) {
+          mbar_arrive_expect_tx(bar, C::kR);
+          bulk_load(to, rp + static_cast<int64_t>(s) * NV * DK, C::kR, bar);
+        } else {
+          mbar_arrive(bar);
+        }
+      }
+      const __nv_bfloat16* p = vp + s * NV;
+#pragma unroll
+      for (int i = 0; i < kChunk / 4; ++i) {
+        const int r = lane / 8 + 4 * i;
+        const bool in = r < d.tokens;
+        cp_async16(to + C::kR + sw128(r, lane % 8), p + static_cast<int64_t>(in ? 4 * i : 0) * a.stride_v - (in ? 0 : lane / 8 * a.stride_v), in);
+      }
+      cp_async_commit();
+      if (s > 0) {
+        cp_async_wait<1>();
+        filled(s - 1);
+      }
+    }
+    cp_async_wait<0>();
+    if (s > 0) filled(s - 1);
+    for (int i = s > C::kRing ? s - C::kRing : 0; i < s; ++i) wait(b_full + 8 * (i % C::kRing), i / C::kRing);
+  } else {  // ---- data
+    const float lg = hp.log2g[h];
+    // rows t = tr + kRows i: each one's rotation is the last one's times a constant step
+    const Turn first = product(load_turn(a.base + (static_cast<int64_t>(blockIdx.x) * 8 + tr / 16) * DK + g * 8),
+                               load_turn(a.offset + (tr % 16) * DK + g * 8));
+    Turn step = load_turn(a.offset + 16 * DK + g * 8);
+    if (kRows == 32) step = product(step, step);
+    __half2 mx = __float2half2_rn(0.f);
+    // q by gamma^(t+1), k by gamma^(127-t)
+    auto convert = [&](uint32_t area, float scale, float grow) {
+      Turn t = scaled(first, scale);
+      const Turn by = scaled(step, grow);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const uint32_t to = area + mine + i * kRows * 128;
+        const Eight y = turned(ld_shared_u4(to), t);
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float2 u = parts(y.first[e]), v = parts(y.second[e]);
+          w[2 * e] = pack_f16x2(u.x, v.x);
+          w[2 * e + 1] = pack_f16x2(u.y, v.y);
+          track(mx, w[2 * e]);
+          track(mx, w[2 * e + 1]);
+        }
+        st_shared_v4(to, w[0], w[1], w[2], w[3]);
+        if (i + 1 < kPer) t = product(t, by);
+      }
+    };
+    cp_async_wait<1>();
+    convert(sq, decay_pow(lg, tr + 1), decay_pow(lg, kRows));
+    cp_async_wait<0>();
+    convert(sk, decay_pow(lg, kChunk - 1 - tr), exp2f(-static_cast<float>(kRows) * lg));
+    report(mx);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(b_qk);
+    const int quarter = warp % 4, row = quarter * 32 + lane, team = warp / 4;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-    {
-      const float back = exp2f(-static_cast<float>(kChunk) * lg);
+    const float back = exp2f(-static_cast<float>(kChunk) * lg);
+    if (wait(b_s, 0)) {
+      tc_fence_after();
 #pragma unroll
-      for (int c = (warp / 4) * 32; c < kChunk; c += (C::kThreads / 128) * 32) {
+      for (int c = team * 32; c < kChunk; c += C::kTeams * 32) {
         uint32_t r[2][16], p[2][16];
         tmem_ld_wait(tS + lanes + c, r);
         const int keep = c < quarter * 32 ? 31 : c > quarter * 32 ? -1 : lane;  // the row's last column here
@@ -699,66 +783,45 @@ __global__ void __launch_bounds__(OutCfg<DK>::kThreads, OutCfg<DK>::kCtas) tc_ou
         tmem_st_wait(tS + lanes + c, p);
       }
       tc_fence_before();
-    }
-    const float f = factor[row];
-    __nv_bfloat16* op = a.o + (static_cast<int64_t>(d.row) + row) * a.stride_o + static_cast<int64_t>(hq) * a.d_v;
-    // Slice s out of its accumulator: 16 columns a thread and turn.
-    auto epilogue = [&](int s) {
-      const uint32_t tO = tm + 128 + (s & 1) * NV;
-#pragma unroll
-      for (int c = (warp / 4) * 16; c < NV; c += (C::kThreads / 128) * 16) {
-        uint32_t r[1][16];
-        tmem_ld_wait(tO + lanes + c, r);
-        uint32_t w[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const __nv_bfloat162 x =
-              __floats2bfloat162_rn(__uint_as_float(r[0][2 * j]) * f, __uint_as_float(r[0][2 * j + 1]) * f);
-          w[j] = *reinterpret_cast<const uint32_t*>(&x);
-        }
-        if (row < d.tokens) {
-          uint4* to = reinterpret_cast<uint4*>(op + s * NV + c);
-          to[0] = make_uint4(w[0], w[1], w[2], w[3]);
-          to[1] = make_uint4(w[4], w[5], w[6], w[7]);
-        }
-      }
-      tc_fence_before();
-    };
-    for (int s = 0; s <= slices; ++s) {
-      if (s < slices) {
-        if (s == 0) cp_async_wait<C::kRing - 1>();
-        else cp_async_wait<C::kRing - 2>();
-        fence_proxy_async_smem();
-        __syncthreads();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(b_p);
+      const float f = factor[row];
+      __nv_bfloat16* op = a.o + (static_cast<int64_t>(d.row) + row) * a.stride_o + static_cast<int64_t>(hq) * a.d_v;
+      const bool in = row < d.tokens, wide = a.o_wide;
+      for (int s = team; s < slices; s += C::kTeams) {
+        if (!done(s)) break;
         tc_fence_after();
-        if (tid == 0) {
-          const uint32_t tO = tm + 128 + (s & 1) * NV;
-          const uint64_t dr = sdesc_sw128(stage(s), DK * 128, 1024), dv = sdesc_sw128(stage(s) + C::kR, kBlock, 1024);
-          if (has_r) {
-            constexpr uint32_t ID = idesc_f16_f32(kChunk, NV, 0, 1);
 #pragma unroll
-            for (int ks = 0; ks < DK / 16; ++ks) mma_f16_ss(tO, dq + kstep(ks), dr + ((ks * 2048) >> 4), ID, ks > 0);
+        for (int c = 0; c < NV; c += 32) {
+          uint32_t r[2][16];
+          tmem_ld_wait(tm + 128 + team * NV + lanes + c, r);
+          if (c + 32 == NV) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(b_read + 8 * team);
           }
-          constexpr uint32_t ID = idesc_bf16_f32(kChunk, NV, 0, 1);
+          if (!in) continue;
 #pragma unroll
-          for (int part = 1; part >= 0; --part)
+          for (int e = 0; e < 2; ++e) {
+            uint32_t w[8];
 #pragma unroll
-            for (int ks = 0; ks < kChunk / 16; ++ks)
-              mma_f16_ts(tO, tS + (ks / 2) * 32 + part * 16 + (ks % 2) * 8, dv + ((ks * 2048) >> 4), ID,
-                         has_r || part == 0 || ks > 0);
-          mma_commit(bo[s & 1]);
+            for (int j = 0; j < 8; ++j) {
+              const __nv_bfloat162 x =
+                  __floats2bfloat162_rn(__uint_as_float(r[e][2 * j]) * f, __uint_as_float(r[e][2 * j + 1]) * f);
+              w[j] = *reinterpret_cast<const uint32_t*>(&x);
+            }
+            __nv_bfloat16* to = op + s * NV + c + e * 16;
+            if (wide) {
+              st_global_v8(to, w);
+            } else {
+              reinterpret_cast<uint4*>(to)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+              reinterpret_cast<uint4*>(to)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            }
+          }
         }
-      }
-      if (s > 0) {
-        dead = !mbar_wait(bo[(s - 1) & 1], ((s - 1) >> 1) & 1, kDrainBudget);
-        if (__syncthreads_or(dead)) break;
-        tc_fence_after();
-        fetch_slice(s - 1 + C::kRing);
-        epilogue(s - 1);
       }
     }
   }
-  cp_async_wait_all();
   tc_fence_before();
   __syncthreads();
   if (warp == 0) {
@@ -863,7 +926,8 @@ cudaError_t launch_packed_tc(const PackedCall& c, const HeadParams& hp, cudaStre
                        static_cast<const __nv_bfloat16*>(c.v), static_cast<__nv_bfloat16*>(c.o), c.pool, desc, base,
                        offset, w, r16, c.cu, units, c.stride_q, c.stride_k, c.stride_v, c.stride_o,
                        static_cast<int32_t>(c.heads_kv), static_cast<int32_t>(c.heads / c.heads_kv),
-                       static_cast<int32_t>(c.d_k), static_cast<int32_t>(c.d_v), c.flags};
+                       static_cast<int32_t>(c.d_k), static_cast<int32_t>(c.d_v), c.flags,
+                       c.stride_o % 16 == 0 && (reinterpret_cast<uintptr_t>(c.o) & 31u) == 0};
   const PackedIndex ix{c.cu, c.slot, c.pos, c.rows, static_cast<int32_t>(c.seqs), static_cast<int32_t>(c.slots), kChunk};
   const cudaError_t e = launch_packed_plan(
       ix, desc, PackedRotation{base, offset, static_cast<int>(c.d_k / 2), (c.flags & RETNET_F_XPOS) != 0}, hp, s);

@@ -190,6 +190,14 @@ __device__ __forceinline__ void prefetch_tensormap(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 
+// Untiled bulk copy global -> this CTA's shared memory (both 16-byte aligned, bytes a multiple of 16),
+// completing on a local mbarrier.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
 // ---- tcgen05: TMEM allocation -----------------------------------------------------------------
 
 __device__ __forceinline__ void tmem_alloc(uint32_t dst_smem, uint32_t ncols) {
@@ -256,6 +264,13 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, int a_mn, in
 __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t addr, uint32_t lbo, uint32_t sbo) {
   return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16) |
          (static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// The same without swizzle, MN-major: 8 x 8 cores of 8 K rows of 16 bytes; `mn` bytes from 8 MN elements
+// to the next 8, `k` bytes from 8 K rows to the next 8.
+__device__ __forceinline__ uint64_t sdesc_cores(uint32_t addr, uint32_t mn, uint32_t k) {
+  return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>((k >> 4) & 0x3FFFu) << 16) |
+         (static_cast<uint64_t>((mn >> 4) & 0x3FFFu) << 32) | (1ull << 46);
 }
 
 // ---- tcgen05: TMEM <-> registers --------------------------------------------------------------
