@@ -19,6 +19,7 @@ The functions carry the C names:
 with the §三.3 normalisations chosen by flags.  Tensors are dense BLHD (see the header).
 """
 import ctypes
+import functools
 import os
 import struct
 
@@ -473,9 +474,11 @@ def retnet_fp16_range_errors(clear=True):
 
 # ---- serving: packed sequences over a pool of states ----------------------------------------
 
-def _address(arr):
-    """Address of a host array as a plain integer (ndarray.ctypes.data_as costs microseconds a call)."""
-    return None if arr is None else arr.__array_interface__["data"][0]
+def _values(a, n):
+    """Host float32 values as bytes, which ctypes passes as their address (the C calls read them before
+    they return; ndarray.ctypes.data_as costs microseconds a call)."""
+    arr = _host_f32(a, n)
+    return None if arr is None else arr.tobytes()
 
 
 def _one_device(*ts):
@@ -493,13 +496,24 @@ def _on(device, fn, stream):
     """fn(raw stream) with ``device`` current (the C calls work on the current device); the stream
     defaults to that device's current one."""
     import torch
+    raw = torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
     if torch.cuda.current_device() == device:
-        status = fn(_stream(stream))
+        status = fn(raw)
     else:
         with torch.cuda.device(device):
-            status = fn(_stream(stream))
+            status = fn(raw)
     if status:
         _check(status)
+
+
+def _allocate(stream, fn):
+    """fn() -- torch.empty calls -- with ``stream`` current, so that the memory is that stream's: free for
+    it to write, and used again behind its work only."""
+    if stream is None:
+        return fn()
+    import torch
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream):
+        return fn()
 
 
 def _token_stride(t, name):
@@ -537,7 +551,11 @@ def _packed_dims(q, k, v, o, pool, seqs):
 
 def retnet_packed_workspace_size(dims) -> int:
     """Bytes of workspace for retnet_retention_packed; dims = (tokens, seqs, heads_kv, d_k, d_v)."""
-    rows, seqs, kv, dk, dv = (int(x) for x in dims)
+    return _packed_workspace_size(*dims)
+
+
+@functools.lru_cache(maxsize=1024)
+def _packed_workspace_size(rows, seqs, kv, dk, dv):
     out = ctypes.c_size_t(0)
     _check(load().retnet_packed_workspace_size(PackedDims(rows, seqs, kv, kv, dk, dv, 1), ctypes.byref(out)))
     return out.value
@@ -559,16 +577,14 @@ def retnet_retention_packed(q, k, v, o, pool, cu_seqlens, slots, pos, gamma, the
     cu = _index(cu_seqlens, torch.int32, seqs + 1, "cu_seqlens")
     sl = _index(slots, torch.int32, seqs, "slots")
     ps = None if pos is None else _index(pos, torch.int64, seqs, "pos")
-    g, th = _host_f32(gamma, d.heads_kv), _host_f32(theta, d.d_k // 2)
+    g, th = _values(gamma, d.heads_kv), _values(theta, d.d_k // 2)
     if workspace is None:
-        workspace = torch.empty(retnet_packed_workspace_size((d.tokens, seqs, d.heads_kv, d.d_k, d.d_v)),
-                                dtype=torch.uint8, device=dev)
-        if stream is not None and not isinstance(stream, int):
-            workspace.record_stream(stream)
+        size = _packed_workspace_size(d.tokens, seqs, d.heads_kv, d.d_k, d.d_v)
+        workspace = _allocate(stream, lambda: torch.empty(size, dtype=torch.uint8, device=dev))
     elif not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     _on(dev, lambda s: load().retnet_retention_packed(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), d, _dtype_code(q), _address(g), _address(th), int(flags),
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), d, _dtype_code(q), g, th, int(flags),
         cu, sl, ps, pool.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(), s), stream)
 
 
@@ -582,9 +598,9 @@ def retnet_retention_step_slots(q, k, v, o, pool, slots, pos, gamma, theta=None,
     d = _packed_dims(q, k, v, o, pool, q.shape[0])
     sl = _index(slots, torch.int32, d.seqs, "slots")
     ps = None if pos is None else _index(pos, torch.int64, d.seqs, "pos")
-    g, th = _host_f32(gamma, d.heads_kv), _host_f32(theta, d.d_k // 2)
+    g, th = _values(gamma, d.heads_kv), _values(theta, d.d_k // 2)
     _on(dev, lambda s: load().retnet_retention_step_slots(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), d, _dtype_code(q), _address(g), _address(th), int(flags),
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), d, _dtype_code(q), g, th, int(flags),
         sl, ps, pool.data_ptr(), s), stream)
 
 
@@ -612,18 +628,19 @@ def retnet_slot_errors(clear=True):
 
 # ---- the MSR epilogue with a learnable affine ------------------------------------------------
 
-def _msr_args(y, weight, bias, *same):
+def _msr_args(y, params, *same):
     import torch
     shape, dtype = y.shape, y.dtype
-    if len(shape) != 3:
-        raise ValueError("y must be (tokens, heads, d_v)")
-    for t in (y, *same):
+    if len(shape) != 3 or not y.is_contiguous():
+        raise ValueError("y must be a contiguous (tokens, heads, d_v)")
+    for t in same:
         if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
             raise ValueError("y, g, out, dout, dy and dg must be contiguous and have one shape and dtype")
-    for t in (weight, bias):
-        if t is not None and (t.shape != shape[1:] or t.dtype != torch.float32 or not t.is_contiguous()):
+    head = shape[1:]
+    for t in params:
+        if t is not None and (t.shape != head or t.dtype != torch.float32 or not t.is_contiguous()):
             raise ValueError("weight, bias, dweight and dbias must be contiguous float32 (heads, d_v)")
-    return _one_device(y, weight, bias, *same)
+    return _one_device(y, *same, *params)
 
 
 def _optional_ptr(t):
@@ -633,15 +650,20 @@ def _optional_ptr(t):
 def retnet_msr_affine(y, g, weight, bias, out, eps=1e-5, stream=None):
     """swish(g) * (weight * GroupNorm_h(y) + bias) into ``out``: y, g, out (tokens, heads, d_v) of one dtype,
     weight and bias (heads, d_v) float32 or None."""
-    dev = _msr_args(y, weight, bias, g, out)
+    dev = _msr_args(y, (weight, bias), g, out)
     _on(dev, lambda s: load().retnet_msr_affine(y.data_ptr(), g.data_ptr(), _optional_ptr(weight), _optional_ptr(bias),
                                                 out.data_ptr(), *y.shape, float(eps), _dtype_code(y), s), stream)
 
 
 def retnet_msr_affine_workspace_size(shape) -> int:
     """Bytes of workspace for retnet_msr_affine_backward; shape = (tokens, heads, d_v)."""
+    return _msr_affine_workspace_size(*shape)
+
+
+@functools.lru_cache(maxsize=1024)
+def _msr_affine_workspace_size(tokens, heads, d_v):
     out = ctypes.c_size_t(0)
-    _check(load().retnet_msr_affine_workspace_size(*(int(x) for x in shape), ctypes.byref(out)))
+    _check(load().retnet_msr_affine_workspace_size(tokens, heads, d_v, ctypes.byref(out)))
     return out.value
 
 
@@ -650,12 +672,10 @@ def retnet_msr_affine_backward(y, g, weight, bias, dout, dy, dg, dweight=None, d
     """Gradient of retnet_msr_affine into dy, dg (shape and dtype of y) and, where given, dweight and dbias
     (heads, d_v) float32.  Without a workspace (uint8 CUDA tensor) one is allocated for the call."""
     import torch
-    dev = _msr_args(y, weight, bias, g, dout, dy, dg)
-    _msr_args(y, dweight, dbias)
+    dev = _msr_args(y, (weight, bias, dweight, dbias), g, dout, dy, dg)
     if workspace is None and (dweight is not None or dbias is not None):
-        workspace = torch.empty(retnet_msr_affine_workspace_size(y.shape), dtype=torch.uint8, device=dev)
-        if stream is not None and not isinstance(stream, int):
-            workspace.record_stream(stream)
+        size = _msr_affine_workspace_size(*y.shape)
+        workspace = _allocate(stream, lambda: torch.empty(size, dtype=torch.uint8, device=dev))
     elif workspace is not None:
         _one_device(y, workspace)
         if not workspace.is_contiguous():
@@ -689,7 +709,7 @@ def retention_parallel(q, k, v, gamma, theta=None, flags=F_ALL, pos0=0, out_dtyp
 
 def msr_affine(y, g, weight=None, bias=None, eps=1e-5, stream=None):
     import torch
-    out = torch.empty_like(y)
+    out = _allocate(stream, lambda: torch.empty_like(y))
     retnet_msr_affine(y, g, weight, bias, out, eps, stream)
     return out
 
@@ -697,7 +717,8 @@ def msr_affine(y, g, weight=None, bias=None, eps=1e-5, stream=None):
 def msr_affine_backward(y, g, weight, bias, dout, eps=1e-5, workspace=None, stream=None):
     """(dy, dg, dweight, dbias) of msr_affine."""
     import torch
-    dy, dg = torch.empty_like(y), torch.empty_like(g)
-    dw, db = (torch.empty(y.shape[1:], dtype=torch.float32, device=y.device) for _ in range(2))
+    dy, dg, sums = _allocate(stream, lambda: (
+        torch.empty_like(y), torch.empty_like(g), torch.empty((2, *y.shape[1:]), dtype=torch.float32, device=y.device)))
+    dw, db = sums.unbind(0)
     retnet_msr_affine_backward(y, g, weight, bias, dout, dy, dg, dw, db, eps, workspace, stream)
     return dy, dg, dw, db

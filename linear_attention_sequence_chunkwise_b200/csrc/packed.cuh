@@ -22,6 +22,7 @@ struct RunDesc {
   int32_t slot;    // the sequence's pool slot
   int64_t pos;     // absolute position of the run's first token
 };
+static_assert(sizeof(RunDesc) == 32, "two 16-byte words");
 
 struct PackedIndex {
   const int32_t* cu;   // [seqs + 1]

@@ -2,6 +2,7 @@
 // (packed.cuh), written on the device because the lengths live there, and the count of sequences
 // that the device refused.
 #include "packed.cuh"
+#include "pdl.cuh"
 
 namespace retnet {
 namespace {
@@ -31,6 +32,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PackedIndex ix, RunDesc*
   __shared__ int total;
   const int tid = threadIdx.x;
   const int64_t u = blockIdx.x;
+  pdl_go();
   if (tid == 0) total = 0;
   int bad = 0, before = 0;
   for (int s0 = 0; s0 < ix.seqs; s0 += kThreads) {
@@ -51,9 +53,9 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PackedIndex ix, RunDesc*
   before = __reduce_add_sync(0xffffffffu, before);
   if (tid % 32 == 0 && before) atomicAdd(&total, before);
   bad = __syncthreads_or(bad);
-  if (rot.offset && u == 0)
-    for (int e = tid; e < 17 * rot.half; e += kThreads)
-      turn(rot.offset + e / rot.half * 2 * rot.half, rot, e / rot.half, e % rot.half, hp);
+  if (rot.offset)  // its rows dealt out to the CTAs
+    for (int64_t r = u; r < 17; r += gridDim.x)
+      for (int j = tid; j < rot.half; j += kThreads) turn(rot.offset + r * 2 * rot.half, rot, r, j, hp);
   const int s = total - 1;  // -1: the first sequence starts behind this unit
   if (bad || s < 0) {
     if (tid == 0) {

@@ -17,6 +17,7 @@
 #include "packed.cuh"
 #include "pdl.cuh"
 #include "sm100_ptx.cuh"
+#include "tensor_map.h"
 
 namespace retnet {
 namespace {
@@ -82,6 +83,18 @@ struct Turn {
 __device__ __forceinline__ Turn load_turn(const float* p) {
   const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(p), s = *reinterpret_cast<const ulonglong2*>(p + 4);
   return Turn{{c.x, c.y}, {s.x, s.y}};
+}
+// (past the L1 cache)
+__device__ __forceinline__ Turn load_turn_l2(const float* p) {
+  const ulonglong2 c = __ldcg(reinterpret_cast<const ulonglong2*>(p)), s = __ldcg(reinterpret_cast<const ulonglong2*>(p + 4));
+  return Turn{{c.x, c.y}, {s.x, s.y}};
+}
+__device__ __forceinline__ RunDesc plan_entry(const RunDesc* p) {
+  const int4 a = __ldcg(reinterpret_cast<const int4*>(p)), b = __ldcg(reinterpret_cast<const int4*>(p) + 1);
+  RunDesc d;
+  d.seq = a.x; d.row = a.y; d.tokens = a.z; d.index = a.w; d.runs = b.x; d.slot = b.y;
+  d.pos = static_cast<int64_t>(static_cast<uint64_t>(static_cast<uint32_t>(b.w)) << 32 | static_cast<uint32_t>(b.z));
+  return d;
 }
 __device__ __forceinline__ Turn scaled(const Turn& t, float f) {
   const Two ff = two(f, f);
@@ -183,8 +196,8 @@ __global__ void __launch_bounds__(256, 2) tc_state_kernel(TcPackedArgs a, HeadPa
   extern __shared__ unsigned char raw_smem[];
   __shared__ uint64_t bar;
   __shared__ uint32_t tmem_at;
-  pdl_go();
   pdl_wait();
+  pdl_go();
   const RunDesc d = a.desc[blockIdx.x];
   if (d.tokens == 0) return;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -308,28 +321,33 @@ __global__ void __launch_bounds__(256, 2) tc_state_kernel(TcPackedArgs a, HeadPa
 // CTA = (sequence, key/value head, up to 128 rows of d_k x NV columns of d_v): the chunks in order, the
 // fp32 state in registers (at most 64 values a thread); before each chunk its fp16 rounding goes to
 // r16, after the last the state goes to the pool.  No W, no scan.  Steps of 64 tokens run through a
-// ring: copies two steps ahead; the data warps cut k of the next step, and add and round the last
-// chunk's state, while a warp of its own issues this step's products (a data warp that issued them
-// held the others up for as long as they ran).
+// ring of three: one warp fetches (TMA: k, v, and the step's rotations), the data warps rotate k and cut
+// it in place and, every second step, add and round the chunk before while the products run, one warp
+// issues the products.  A data warp that also issued them held the others up for as long as they ran.
 template <int M, int NV>
 struct SeqCfg {
   static constexpr int kData = NV == 256 ? 512 : 256;
-  static constexpr int kThreads = kData + 32;
+  static constexpr int kThreads = kData + 128;    // a warpgroup for the copying and the issuing warp
   static constexpr int kHold = NV * 128 / kData;  // state values a thread
   static constexpr int kStep = 64;
-  static constexpr int kPlane = kStep * M * 2, kVBytes = kStep * NV * 2;
-  static constexpr int kSmem = 3 * kPlane + 4 * kPlane + 3 * kVBytes + 1024;
+  static constexpr int kPlane = kStep * M * 2, kVBytes = kStep * NV * 2, kTurns = kStep / 16 * M * 4;
+  static constexpr int kSmem = 3 * kPlane + 4 * kPlane + 3 * kVBytes + 3 * kTurns + 1024;
   static constexpr int kCols = 2 * NV;
+  // 640 threads are launched with 96 registers each (61440); 512 x 112 + 128 x 24 = 60416 of them
+  static constexpr bool kMoveRegisters = kData == 512;
 };
 
 template <int M, int NV>
-__global__ void __launch_bounds__(SeqCfg<M, NV>::kThreads, 1) tc_sequence_kernel(TcPackedArgs a, HeadParams hp) {
+__global__ void __launch_bounds__(SeqCfg<M, NV>::kThreads, 1)
+    tc_sequence_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, TcPackedArgs a,
+                       HeadParams hp) {
   using C = SeqCfg<M, NV>;
   extern __shared__ unsigned char raw_smem[];
-  __shared__ uint64_t bars[4];  // products of even / odd steps done; operands of even / odd steps ready
+  // products of even / odd steps done; operands of even / odd steps ready; ring slots filled, free
+  __shared__ uint64_t bars[10];
   __shared__ uint32_t tmem_at;
-  pdl_go();
   pdl_wait();
+  pdl_go();
   const int seq = blockIdx.x, h = blockIdx.y, slices = a.d_v / NV;
   const int64_t u0 = a.cu[seq] / kChunk + seq;
   if (u0 < 0 || u0 >= a.units) return;  // cu_seqlens out of order: no run has tokens
@@ -338,16 +356,22 @@ __global__ void __launch_bounds__(SeqCfg<M, NV>::kThreads, 1) tc_sequence_kernel
   const int len = (d.runs - 1) * kChunk + a.desc[u0 + d.runs - 1].tokens, steps = (len + C::kStep - 1) / C::kStep;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int k0 = (blockIdx.z / slices) * M, v0 = (blockIdx.z % slices) * NV;
-  const uint32_t sm = (smem_addr(raw_smem) + 1023u) & ~1023u, s2 = sm + 3 * C::kPlane, sv = s2 + 4 * C::kPlane;
-  const uint32_t done = smem_addr(&bars[0]), ready = smem_addr(&bars[2]);
+  const uint32_t sm = (smem_addr(raw_smem) + 1023u) & ~1023u, s2 = sm + 3 * C::kPlane, sv = s2 + 4 * C::kPlane,
+                 st_turns = sv + 3 * C::kVBytes;
+  const uint32_t b_done = smem_addr(&bars[0]), b_ready = smem_addr(&bars[2]), b_full = smem_addr(&bars[4]),
+                 b_free = smem_addr(&bars[7]);
   if (warp == 0) {
     tmem_alloc(smem_addr(&tmem_at), C::kCols);
     tmem_relinquish();
   }
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(done + 8 * i, 1);
-      mbar_init(ready + 8 * i, C::kData / 32);
+      mbar_init(b_done + 8 * i, 1);
+      mbar_init(b_ready + 8 * i, C::kData / 32);
+    }
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(b_full + 8 * i, 1);
+      mbar_init(b_free + 8 * i, 1);
     }
     fence_mbar_init();
   }
@@ -355,65 +379,66 @@ __global__ void __launch_bounds__(SeqCfg<M, NV>::kThreads, 1) tc_sequence_kernel
   __syncthreads();
   tc_fence_after();
   const uint32_t tm = tmem_at;
-  auto slot_of = [&](int st) { return st % 3; };
-  auto products_done = [&](int st) { return mbar_wait(done + 8 * (st & 1), (st >> 1) & 1, kDrainBudget); };
+  auto slot_of = [](int st) { return st % 3; };
+  auto products_done = [&](int st) { return mbar_wait(b_done + 8 * (st & 1), (st >> 1) & 1, kDrainBudget); };
+  auto filled = [&](int st) { return mbar_wait(b_full + 8 * slot_of(st), (st / 3) & 1, kDrainBudget); };
 
-  if (warp == C::kData / 32) {
-    if (lane == 0) {
-      constexpr uint32_t ID = idesc_bf16_f32(M, NV, 1, 1);
-      int st = 0;
-      for (; st < steps; ++st) {
-        if (!mbar_wait(ready + 8 * (st & 1), (st >> 1) & 1, kDrainBudget)) break;
-        tc_fence_after();
-        const uint64_t dv = sdesc_sw128(sv + slot_of(st) * C::kVBytes, C::kStep * 128, 1024);
-        const uint64_t d0 = sdesc_sw128(sm + slot_of(st) * C::kPlane, C::kStep * 128, 1024);
-        const uint64_t d1 = sdesc_sw128(s2 + (st & 1) * 2 * C::kPlane, C::kStep * 128, 1024);
-        const uint32_t tD = tm + ((st >> 1) & 1) * NV;
+  if (tid >= C::kData) {
+    if constexpr (C::kMoveRegisters) registers_less<24>();
+    if (warp == C::kData / 32) {  // ---- products
+      if (lane == 0) {
+        constexpr uint32_t ID = idesc_bf16_f32(M, NV, 1, 1);
+        int st = 0;
+        for (; st < steps; ++st) {
+          if (!mbar_wait(b_ready + 8 * (st & 1), (st >> 1) & 1, kDrainBudget)) break;
+          tc_fence_after();
+          const uint64_t dv = sdesc_sw128(sv + slot_of(st) * C::kVBytes, C::kStep * 128, 1024);
+          const uint64_t d0 = sdesc_sw128(sm + slot_of(st) * C::kPlane, C::kStep * 128, 1024);
+          const uint64_t d1 = sdesc_sw128(s2 + (st & 1) * 2 * C::kPlane, C::kStep * 128, 1024);
+          const uint32_t tD = tm + ((st >> 1) & 1) * NV;
 #pragma unroll
-        for (int p = 2; p >= 0; --p) {  // the small planes first
-          const uint64_t dk = p == 0 ? d0 : d1 + (((p - 1) * C::kPlane) >> 4);
+          for (int p = 2; p >= 0; --p) {  // the small planes first
+            const uint64_t dk = p == 0 ? d0 : d1 + (((p - 1) * C::kPlane) >> 4);
 #pragma unroll
-          for (int ks = 0; ks < C::kStep / 16; ++ks)
-            mma_f16_ss(tD, dk + ((ks * 2048) >> 4), dv + ((ks * 2048) >> 4), ID, st % 2 || p < 2 || ks > 0);
+            for (int ks = 0; ks < C::kStep / 16; ++ks)
+              mma_f16_ss(tD, dk + ((ks * 2048) >> 4), dv + ((ks * 2048) >> 4), ID, st % 2 || p < 2 || ks > 0);
+          }
+          mma_commit(b_done + 8 * (st & 1));
+          mma_commit(b_free + 8 * slot_of(st));
         }
-        mma_commit(done + 8 * (st & 1));
+        for (int i = st > 3 ? st - 3 : 0; i < st; ++i) mbar_wait(b_free + 8 * slot_of(i), (i / 3) & 1, kDrainBudget);
       }
-      if (st > 0) products_done(st - 1);
+    } else if (warp == C::kData / 32 + 1) {  // ---- copies
+      if (lane == 0) {
+        int st = 0;
+        for (; st < steps; ++st) {
+          const int slot = slot_of(st);
+          if (st >= 3 && !mbar_wait(b_free + 8 * slot, (st / 3 - 1) & 1, kDrainBudget)) break;
+          const uint32_t bar = b_full + 8 * slot;
+          mbar_arrive_expect_tx(bar, C::kPlane + C::kVBytes + C::kTurns);
+          const int row = d.row + st * C::kStep;
+#pragma unroll
+          for (int c = 0; c < M; c += 64)
+            tma_load_2d(sm + slot * C::kPlane + c * (C::kStep * 2), &map_k, bar, h * a.d_k + k0 + c, row);
+#pragma unroll
+          for (int c = 0; c < NV; c += 64)
+            tma_load_2d(sv + slot * C::kVBytes + c * (C::kStep * 2), &map_v, bar, h * a.d_v + v0 + c, row);
+#pragma unroll
+          for (int i = 0; i < C::kStep / 16; ++i)
+            bulk_load(st_turns + slot * C::kTurns + i * M * 4,
+                      a.base + (u0 * 8 + st * (C::kStep / 16) + i) * static_cast<int64_t>(a.d_k) + k0, M * 4, bar);
+        }
+        for (int i = st > 3 ? st - 3 : 0; i < st; ++i) filled(i);  // no copy in flight at the end
+      }
     }
-  } else {
+  } else {  // ---- data
+    if constexpr (C::kMoveRegisters) registers_more<112>();
     constexpr int kGroups = M / 8, kRows = C::kData / kGroups, kPer = C::kStep / kRows;
     static_assert(kRows % 16 == 0, "a thread's rows share their place in a group of 16 tokens");
     const int g = tid % kGroups, tr = tid / kGroups;
-    const __nv_bfloat16* kp = a.k + static_cast<int64_t>(d.row) * a.stride_k + static_cast<int64_t>(h) * a.d_k + k0 + g * 8;
-    const __nv_bfloat16* vp = a.v + static_cast<int64_t>(d.row) * a.stride_v + static_cast<int64_t>(h) * a.d_v + v0;
     const uint32_t mine = (g / 8) * (C::kStep * 128) + sw128(tr, g % 8);  // kRows more rows: kRows * 128 bytes on
-    constexpr int kVPer = C::kStep * (NV / 8) / C::kData, kVRows = C::kData / (NV / 8);
-    const int vr = tid / (NV / 8), vc = tid % (NV / 8);
-    static_assert(kVRows % 8 == 0, "rows kVRows apart are swizzled alike");
-    const uint32_t v_mine = (vc / 8) * (C::kStep * 128) + sw128(vr, vc % 8);
-    auto fetch = [&](int st) {
-      if (st < steps) {
-        const uint32_t tk = sm + slot_of(st) * C::kPlane + mine, tv = sv + slot_of(st) * C::kVBytes + v_mine;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const int t = st * C::kStep + tr + i * kRows;
-          const bool in = t < len;
-          cp_async16(tk + i * kRows * 128, kp + static_cast<int64_t>(in ? t : 0) * a.stride_k, in);
-        }
-#pragma unroll
-        for (int i = 0; i < kVPer; ++i) {
-          const int t = st * C::kStep + vr + i * kVRows;
-          const bool in = t < len;
-          cp_async16(tv + i * kVRows * 128, vp + static_cast<int64_t>(in ? t : 0) * a.stride_v + vc * 8, in);
-        }
-      }
-      cp_async_commit();
-    };
-    fetch(0);
-    fetch(1);
     const float lg = hp.log2g[h];
     const Turn off = scaled(load_turn(a.offset + (tr % 16) * a.d_k + k0 + g * 8), decay_pow(lg, 15 - tr % 16));
-    const float* base = a.base + u0 * 8 * a.d_k + k0 + g * 8;
     // this thread's piece of the state: row (k0 + row), columns v0 + cols on
     const int quarter = warp % 4, cols = v0 + (warp / 4) * C::kHold;
     const bool holds = M == 128 || lane < 16;
@@ -444,44 +469,55 @@ __global__ void __launch_bounds__(SeqCfg<M, NV>::kThreads, 1) tc_sequence_kernel
     if (d.pos > 0) emit(0);
     // S <- S + less S + up D, D the products of a chunk
     auto add_chunk = [&](int chunk, float less, float up) {
+      tc_fence_after();
 #pragma unroll
-      for (int e = 0; e < C::kHold; e += 32) {
-        uint32_t r[2][16];
+      for (int e = 0; e < C::kHold; e += 16) {
+        uint32_t r[1][16];
         tmem_ld_wait(tm + (static_cast<uint32_t>(quarter * 32) << 16) + (chunk & 1) * NV + (warp / 4) * C::kHold + e, r);
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-          S[e + j] = fmaf(less, S[e + j], fmaf(up, __uint_as_float(r[j / 16][j % 16]), S[e + j]));
+        for (int j = 0; j < 16; ++j) S[e + j] = fmaf(less, S[e + j], fmaf(up, __uint_as_float(r[0][j]), S[e + j]));
       }
       tc_fence_before();
     };
     const float full_less = decay_less_one(lg, kChunk);
     bool alive = true;
     for (int st = 0; st < steps; ++st) {
-      cp_async_wait<1>();
-      const uint32_t hi = sm + slot_of(st) * C::kPlane + mine, low = s2 + (st & 1) * 2 * C::kPlane + mine;
+      // the step's copies have landed; the small planes of two steps ago have been read
+      if (!(alive = (st < 2 || products_done(st - 2)) && filled(st))) break;
+      const int slot = slot_of(st), left = len - st * C::kStep;
+      const uint32_t hi = sm + slot * C::kPlane + mine, low = s2 + (st & 1) * 2 * C::kPlane + mine;
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        const int at = st * (C::kStep / 16) + (tr + i * kRows) / 16;  // base rows of a chunk are 8, in order
+        const int t = tr + i * kRows;
         const uint32_t o = i * kRows * 128;
-        Eight y = turned(ld_shared_u4(hi + o), product(scaled(load_turn(base + static_cast<int64_t>(at) * a.d_k),
-                                                              decay_pow(lg, 112 - 16 * (at % 8))), off));
+        const uint32_t at = st_turns + slot * C::kTurns + (t / 16) * (M * 4) + g * 32;
+        const uint4 c = ld_shared_u4(at), s = ld_shared_u4(at + 16);
+        const Turn base{{static_cast<Two>(c.y) << 32 | c.x, static_cast<Two>(c.w) << 32 | c.z},
+                        {static_cast<Two>(s.y) << 32 | s.x, static_cast<Two>(s.w) << 32 | s.z}};
+        uint4 raw = ld_shared_u4(hi + o);
+        if (t >= left) raw = make_uint4(0, 0, 0, 0);  // rows behind the sequence
+        Eight y = turned(raw, product(scaled(base, decay_pow(lg, 112 - 64 * (st & 1) - t / 16 * 16)), off));
         store_plane(hi + o, y);
         store_plane(low + o, y);
         store_plane(low + C::kPlane + o, y);
       }
+      if (left < C::kStep) {  // 0 x v of another sequence may not be 0
+        for (int e = tid; e < (C::kStep - left) * (NV / 8); e += C::kData)
+          st_shared_v4(sv + slot * C::kVBytes + (e % (NV / 8) / 8) * (C::kStep * 128) + (left + e / (NV / 8)) * 128 + e % 8 * 16, 0, 0, 0, 0);
+      }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(ready + 8 * (st & 1));
-      if (st > 0 && !(alive = products_done(st - 1))) break;  // its ring slot and small planes are free
-      fetch(st + 2);
-      if (st > 0 && st % 2 == 0) {  // the chunk before this step is complete
-        tc_fence_after();
+      if (lane == 0) mbar_arrive(b_ready + 8 * (st & 1));
+      if (st >= 3 && st % 2) {  // (awaited above) the products of chunk st / 2 - 1
         add_chunk(st / 2 - 1, full_less, 1.f);
         emit(st / 2);
       }
     }
+    if (alive && steps % 2 && steps > 1 && (alive = products_done(steps - 2))) {
+      add_chunk(d.runs - 2, full_less, 1.f);
+      emit(d.runs - 1);
+    }
     if (alive && products_done(steps - 1)) {
-      tc_fence_after();
       const int last = len - (d.runs - 1) * kChunk;
       add_chunk(d.runs - 1, decay_less_one(lg, last), exp2f(static_cast<float>(last - kChunk) * lg));
       if (holds) {
@@ -491,7 +527,6 @@ __global__ void __launch_bounds__(SeqCfg<M, NV>::kThreads, 1) tc_sequence_kernel
       }
     }
     report(mx);
-    cp_async_wait<0>();
   }
   tc_fence_before();
   __syncthreads();
@@ -507,8 +542,8 @@ __global__ void __launch_bounds__(SeqCfg<M, NV>::kThreads, 1) tc_sequence_kernel
 // gamma^(len-128) <= 2^12.
 constexpr int kScanThreads = 256;
 __global__ void __launch_bounds__(kScanThreads) tc_scan_kernel(TcPackedArgs a, HeadParams hp) {
-  pdl_go();
   pdl_wait();
+  pdl_go();
   const int s = blockIdx.z, h = blockIdx.y;
   const int64_t n4 = static_cast<int64_t>(a.d_k) * a.d_v / 4;
   const int64_t e = static_cast<int64_t>(blockIdx.x) * kScanThreads + threadIdx.x;
@@ -591,9 +626,14 @@ __global__ void __launch_bounds__(OutCfg<DK>::kThreads, OutCfg<DK>::kCtas) tc_ou
   __shared__ uint64_t bars[3 + C::kRing + 2 * C::kTeams];
   __shared__ uint32_t tmem_at;
   __shared__ float factor[kChunk];
-  pdl_wait();
-  const RunDesc d = a.desc[blockIdx.x];
-  if (d.tokens == 0) return;
+  // This grid starts when the state kernel before it has passed its own wait, so the plan is complete;
+  // it is read past the L1 cache.  The states are not: the copying warp waits before it fetches R (and
+  // before the CTA ends, so that no later kernel runs beside the state kernel).
+  const RunDesc d = plan_entry(a.desc + blockIdx.x);
+  if (d.tokens == 0) {
+    pdl_wait();
+    return;
+  }
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int hq = blockIdx.y, h = hq / a.group, slices = a.d_v / NV;
   const uint32_t sq = (smem_addr(raw_smem) + 1023u) & ~1023u, sk = sq + C::kQ, own = sk + C::kQ;
@@ -694,6 +734,7 @@ __global__ void __launch_bounds__(OutCfg<DK>::kThreads, OutCfg<DK>::kCtas) tc_ou
       __syncwarp();
       if (lane == 0) mbar_arrive(b_full + 8 * (s % C::kRing));
     };
+    pdl_wait();
     bool ok = true;
     int s = 0;
     for (; s < slices; ++s) {
@@ -728,9 +769,9 @@ __global__ void __launch_bounds__(OutCfg<DK>::kThreads, OutCfg<DK>::kCtas) tc_ou
   } else {  // ---- data
     const float lg = hp.log2g[h];
     // rows t = tr + kRows i: each one's rotation is the last one's times a constant step
-    const Turn first = product(load_turn(a.base + (static_cast<int64_t>(blockIdx.x) * 8 + tr / 16) * DK + g * 8),
-                               load_turn(a.offset + (tr % 16) * DK + g * 8));
-    Turn step = load_turn(a.offset + 16 * DK + g * 8);
+    const Turn first = product(load_turn_l2(a.base + (static_cast<int64_t>(blockIdx.x) * 8 + tr / 16) * DK + g * 8),
+                               load_turn_l2(a.offset + (tr % 16) * DK + g * 8));
+    Turn step = load_turn_l2(a.offset + 16 * DK + g * 8);
     if (kRows == 32) step = product(step, step);
     __half2 mx = __float2half2_rn(0.f);
     // q by gamma^(t+1), k by gamma^(127-t)
@@ -842,10 +883,14 @@ cudaError_t launch_sequences(const PackedCall& c, const TcPackedArgs& a, const H
   using C = SeqCfg<M, NV>;
   const cudaError_t e = prepare(tc_sequence_kernel<M, NV>, C::kSmem);
   if (e != cudaSuccess) return e;
+  CUtensorMap mk, mv;
+  if (!encode_token_rows(&mk, c.k, c.rows, c.heads_kv * c.d_k, c.stride_k, C::kStep) ||
+      !encode_token_rows(&mv, c.v, c.rows, c.heads_kv * c.d_v, c.stride_v, C::kStep))
+    return cudaErrorUnknown;
   return launch_dependent(tc_sequence_kernel<M, NV>,
                           dim3(static_cast<unsigned>(c.seqs), static_cast<unsigned>(a.kv),
                                static_cast<unsigned>((a.d_k / M) * (a.d_v / NV))),
-                          dim3(C::kThreads), C::kSmem, s, a, hp);
+                          dim3(C::kThreads), C::kSmem, s, mk, mv, a, hp);
 }
 template <int M, int NV>
 cudaError_t launch_chunks(const PackedCall& c, const TcPackedArgs& a, const HeadParams& hp, cudaStream_t s) {
@@ -861,12 +906,14 @@ cudaError_t launch_chunks(const PackedCall& c, const TcPackedArgs& a, const Head
   return launch_dependent(tc_scan_kernel, dim3(nb, kv, static_cast<unsigned>(c.seqs)), dim3(kScanThreads), 0, s, a, hp);
 }
 
-// Whether the states are walked sequence by sequence.  Chunk by chunk takes one more pass over every
-// chunk's fp32 state, written and read (at d_k 256, d_v 512 more bytes than q, k, v and o together);
-// a sequence's walk takes the time of its longest one, so it needs enough CTAs to fill the GPU.
+// Whether the states are walked sequence by sequence.  Chunk by chunk takes one more launch and one
+// more pass over every chunk's fp32 state, written and read (at d_k 256, d_v 512 more bytes than q, k,
+// v and o together); a sequence's walk takes the time of its longest one, so it needs enough CTAs to
+// fill the GPU, or sequences short enough (two chunks on average) that there is nothing to spread.
 int sequence_columns(int64_t d_v) { return d_v % 256 == 0 ? 256 : d_v % 128 == 0 ? 128 : 64; }
-bool by_sequence(int64_t seqs, int64_t heads_kv, int64_t d_k, int64_t d_v) {
-  return seqs * heads_kv * (d_k > 128 ? d_k / 128 : 1) * (d_v / sequence_columns(d_v)) >= 96;
+bool by_sequence(int64_t rows, int64_t seqs, int64_t heads_kv, int64_t d_k, int64_t d_v) {
+  return rows <= 2 * kChunk * seqs ||
+         seqs * heads_kv * (d_k > 128 ? d_k / 128 : 1) * (d_v / sequence_columns(d_v)) >= 96;
 }
 
 template <int DK>
@@ -875,7 +922,7 @@ cudaError_t launch_shape(const PackedCall& c, const TcPackedArgs& a, const HeadP
   using O = OutCfg<DK>;
   cudaError_t e = prepare(tc_output_kernel<DK>, O::kSmem);
   if (e != cudaSuccess) return e;
-  if (by_sequence(c.seqs, c.heads_kv, c.d_k, c.d_v)) {
+  if (by_sequence(c.rows, c.seqs, c.heads_kv, c.d_k, c.d_v)) {
     const int nv = sequence_columns(c.d_v);
     e = nv == 256 ? launch_sequences<M, 256>(c, a, hp, s)
                   : nv == 128 ? launch_sequences<M, 128>(c, a, hp, s) : launch_sequences<M, 64>(c, a, hp, s);
@@ -903,7 +950,7 @@ bool packed_tc_supported(const PackedCall& c, const HeadParams& hp) {
 size_t packed_tc_workspace_bytes(int64_t rows, int64_t seqs, int64_t heads_kv, int64_t d_k, int64_t d_v) {
   const size_t units = static_cast<size_t>(packed_units(rows, seqs, kChunk));
   const size_t states = units * static_cast<size_t>(heads_kv * d_k * d_v);
-  const bool chunks = d_v < 64 || !by_sequence(seqs, heads_kv, d_k, d_v);
+  const bool chunks = d_v < 64 || !by_sequence(rows, seqs, heads_kv, d_k, d_v);
   return 256 + a256(sizeof(RunDesc) * units) + a256(sizeof(float) * units * 8 * static_cast<size_t>(d_k)) +
          a256(sizeof(float) * 17 * static_cast<size_t>(d_k)) + (chunks ? a256(sizeof(float) * states) : 0) + sizeof(__half) * states;
 }
@@ -920,7 +967,7 @@ cudaError_t launch_packed_tc(const PackedCall& c, const HeadParams& hp, cudaStre
   float* base = reinterpret_cast<float*>(take(sizeof(float) * units * 8 * c.d_k));
   float* offset = reinterpret_cast<float*>(take(sizeof(float) * 17 * c.d_k));
   const size_t states = static_cast<size_t>(units * c.heads_kv * c.d_k * c.d_v);
-  float* w = by_sequence(c.seqs, c.heads_kv, c.d_k, c.d_v) ? nullptr : reinterpret_cast<float*>(take(sizeof(float) * states));
+  float* w = by_sequence(c.rows, c.seqs, c.heads_kv, c.d_k, c.d_v) ? nullptr : reinterpret_cast<float*>(take(sizeof(float) * states));
   __half* r16 = reinterpret_cast<__half*>(take(sizeof(__half) * states));
   const TcPackedArgs a{static_cast<const __nv_bfloat16*>(c.q), static_cast<const __nv_bfloat16*>(c.k),
                        static_cast<const __nv_bfloat16*>(c.v), static_cast<__nv_bfloat16*>(c.o), c.pool, desc, base,

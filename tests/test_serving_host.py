@@ -19,7 +19,7 @@ def lib():
 
 
 def _fp(a):
-    return rn._address(a)
+    return a.tobytes()
 
 
 def _dims(**kw):
@@ -138,6 +138,6 @@ def test_binding_refusals():
         rn._index(sl, torch.int32, 3, "slots")
     y = torch.zeros(3, 2, 8)
     with pytest.raises(ValueError, match="one shape"):
-        rn._msr_args(y, None, None, y[:, :, :4])
+        rn._msr_args(y, (None, None), y[:, :, :4])
     with pytest.raises(ValueError, match="float32"):
-        rn._msr_args(y, torch.zeros(8), None, y)
+        rn._msr_args(y, (torch.zeros(8), None), y)
