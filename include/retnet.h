@@ -475,7 +475,7 @@ RETNET_API retnet_status_t retnet_retention_packed(const void* q, const void* k,
                                         const int32_t* slots, const int64_t* pos, float* pool,
                                         void* workspace, size_t workspace_bytes, void* stream);
 
-/* Workspace bytes of retnet_retention_packed (strides, heads and slots are not read). */
+/* Workspace bytes of retnet_retention_packed (strides and slots are not read). */
 RETNET_API retnet_status_t retnet_packed_workspace_size(retnet_packed_t dims, size_t* bytes);
 
 /*

@@ -550,14 +550,14 @@ def _packed_dims(q, k, v, o, pool, seqs):
 
 
 def retnet_packed_workspace_size(dims) -> int:
-    """Bytes of workspace for retnet_retention_packed; dims = (tokens, seqs, heads_kv, d_k, d_v)."""
+    """Bytes of workspace for retnet_retention_packed; dims = (tokens, seqs, heads, heads_kv, d_k, d_v)."""
     return _packed_workspace_size(*dims)
 
 
 @functools.lru_cache(maxsize=1024)
-def _packed_workspace_size(rows, seqs, kv, dk, dv):
+def _packed_workspace_size(rows, seqs, heads, kv, dk, dv):
     out = ctypes.c_size_t(0)
-    _check(load().retnet_packed_workspace_size(PackedDims(rows, seqs, kv, kv, dk, dv, 1), ctypes.byref(out)))
+    _check(load().retnet_packed_workspace_size(PackedDims(rows, seqs, heads, kv, dk, dv, 1), ctypes.byref(out)))
     return out.value
 
 
@@ -579,7 +579,7 @@ def retnet_retention_packed(q, k, v, o, pool, cu_seqlens, slots, pos, gamma, the
     ps = None if pos is None else _index(pos, torch.int64, seqs, "pos")
     g, th = _values(gamma, d.heads_kv), _values(theta, d.d_k // 2)
     if workspace is None:
-        size = _packed_workspace_size(d.tokens, seqs, d.heads_kv, d.d_k, d.d_v)
+        size = _packed_workspace_size(d.tokens, seqs, d.heads, d.heads_kv, d.d_k, d.d_v)
         workspace = _allocate(stream, lambda: torch.empty(size, dtype=torch.uint8, device=dev))
     elif not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")

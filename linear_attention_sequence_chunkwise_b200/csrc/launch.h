@@ -162,7 +162,7 @@ struct PackedCall {
 // pointers on 16-byte boundaries, gamma^128 >= 2^-12 for every head, no RETNET_F_PRECISE.
 bool packed_tc_supported(const PackedCall& c, const HeadParams& hp);
 // Bytes of workspace of the two kernel families.
-size_t packed_simt_workspace_bytes(int64_t rows, int64_t seqs, int64_t heads_kv, int64_t d_k, int64_t d_v);
+size_t packed_simt_workspace_bytes(int64_t rows, int64_t seqs, int64_t heads, int64_t heads_kv, int64_t d_k, int64_t d_v);
 size_t packed_tc_workspace_bytes(int64_t rows, int64_t seqs, int64_t heads_kv, int64_t d_k, int64_t d_v);
 cudaError_t launch_packed_tc(const PackedCall& c, const HeadParams& hp, cudaStream_t s);
 cudaError_t packed_wait_timeouts(unsigned int* count, bool clear);

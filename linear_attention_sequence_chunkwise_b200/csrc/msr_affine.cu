@@ -12,6 +12,9 @@
 // rate), and the gradient's dw and db, sums over all tokens, are kept in registers, added up over the
 // CTA in shared memory and written as one partial row a CTA; a second kernel adds the partial rows in
 // order (no atomics: the same sums every time).
+#include <algorithm>
+
+#include "fp32x2.cuh"
 #include "launch.h"
 #include "pdl.cuh"
 
@@ -38,9 +41,10 @@ template <>
 struct Raw<__nv_bfloat16> {
   uint32_t x[4];
 };
-__device__ __forceinline__ float value(const Raw<float>& r, int e) { return r.x[e]; }
-__device__ __forceinline__ float value(const Raw<__nv_bfloat16>& r, int e) {
-  return __uint_as_float(e % 2 ? r.x[e / 2] & 0xffff0000u : r.x[e / 2] << 16);
+// Values 2 i and 2 i + 1.
+__device__ __forceinline__ Two value2(const Raw<float>& r, int i) { return two(r.x[2 * i], r.x[2 * i + 1]); }
+__device__ __forceinline__ Two value2(const Raw<__nv_bfloat16>& r, int i) {
+  return two(__uint_as_float(r.x[i] << 16), __uint_as_float(r.x[i] & 0xffff0000u));
 }
 
 template <int W, int LPR>
@@ -83,8 +87,18 @@ __device__ __forceinline__ void load(Raw<__nv_bfloat16>& r, const __nv_bfloat16*
     }
   }
 }
+__device__ __forceinline__ void spread(const Two (&v)[4], float (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 p = parts(v[i]);
+    x[2 * i] = p.x;
+    x[2 * i + 1] = p.y;
+  }
+}
 template <int W, int LPR>
-__device__ __forceinline__ void store(float* p, int lane, int m, int d_v, const float (&x)[8]) {
+__device__ __forceinline__ void store(float* p, int lane, int m, int d_v, const Two (&v)[4]) {
+  float x[8];
+  spread(v, x);
 #pragma unroll
   for (int e = 0; e < 8; e += W == 1 ? 1 : 4) {
     const int c = column<W, LPR>(lane, m, e);
@@ -98,7 +112,9 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 template <int W, int LPR>
-__device__ __forceinline__ void store(__nv_bfloat16* p, int lane, int m, int d_v, const float (&x)[8]) {
+__device__ __forceinline__ void store(__nv_bfloat16* p, int lane, int m, int d_v, const Two (&v)[4]) {
+  float x[8];
+  spread(v, x);
 #pragma unroll
   for (int e = 0; e < 8; e += W) {
     const int c = column<W, LPR>(lane, m, e);
@@ -119,32 +135,41 @@ __device__ __forceinline__ float row_sum(float x) {
   return x;
 }
 
-// Mean and 1/sd of the row in x (values past d_v are zero and stay out of the variance).
-template <int MG, int W, int LPR>
-__device__ __forceinline__ void row_stats(const float (&x)[MG][8], int lane, int d_v, float eps, float& mean, float& inv) {
-  float s = 0.f;
+// x <- x - mean, and 1/sd (values past d_v, loaded as zeros, become zeros: out of the variance).  FULL:
+// the lanes hold exactly d_v values.
+template <int MG, int W, int LPR, bool FULL>
+__device__ __forceinline__ float centre(Two (&x)[MG][4], int lane, int d_v, float inv_n, float eps) {
+  Two s = two(0.f);
 #pragma unroll
   for (int m = 0; m < MG; ++m)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) s += x[m][e];
-  mean = row_sum<LPR>(s) / static_cast<float>(d_v);
-  float sq = 0.f;
+    for (int i = 0; i < 4; ++i) s = add2(s, x[m][i]);
+  const Two less = two(-row_sum<LPR>(sum_of(s)) * inv_n);
+  Two sq = two(0.f);
 #pragma unroll
   for (int m = 0; m < MG; ++m)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float c = column<W, LPR>(lane, m, e) < d_v ? x[m][e] - mean : 0.f;
-      sq = fmaf(c, c, sq);
+    for (int i = 0; i < 4; ++i) {
+      x[m][i] = add2(x[m][i], less);
+      if (!FULL) {
+        const float2 p = parts(x[m][i]);
+        x[m][i] = two(column<W, LPR>(lane, m, 2 * i) < d_v ? p.x : 0.f, column<W, LPR>(lane, m, 2 * i + 1) < d_v ? p.y : 0.f);
+      }
+      sq = fma2(x[m][i], x[m][i], sq);
     }
-  inv = rsqrtf(row_sum<LPR>(sq) / static_cast<float>(d_v) + eps);
+  return rsqrtf(fmaf(row_sum<LPR>(sum_of(sq)), inv_n, eps));
 }
 
-// (the approximate division is within 2 ulp, and 0 where exp passes 2^126, as the quotient nearly is)
-__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.f, 1.f + expf(-g)); }
+// 1 / (1 + exp(-g)) of both lanes by the approximate exponential and division: a few 2^-23 of the value
+// for |g| below ten, growing with |g| where 1 + exp(-g) is near 1 or the product with g is tiny.
+__device__ __forceinline__ Two sigmoid2(Two g) {
+  const float2 p = parts(g);
+  return two(__fdividef(1.f, 1.f + __expf(-p.x)), __fdividef(1.f, 1.f + __expf(-p.y)));
+}
 
 // Weight and bias of the CTA's head.
 template <int MG, int W, int LPR>
-__device__ __forceinline__ void load_affine(float (&w)[MG][8], float (&b)[MG][8], const float* weight, const float* bias,
+__device__ __forceinline__ void load_affine(Two (&w)[MG][4], Two (&b)[MG][4], const float* weight, const float* bias,
                                             int h, int lane, int d_v) {
 #pragma unroll
   for (int m = 0; m < MG; ++m) {
@@ -152,52 +177,53 @@ __device__ __forceinline__ void load_affine(float (&w)[MG][8], float (&b)[MG][8]
     if (weight) load<W, LPR>(rw, weight + static_cast<int64_t>(h) * d_v, lane, m, d_v);
     if (bias) load<W, LPR>(rb, bias + static_cast<int64_t>(h) * d_v, lane, m, d_v);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      w[m][e] = weight ? rw.x[e] : 1.f;
-      b[m][e] = bias ? rb.x[e] : 0.f;
+    for (int i = 0; i < 4; ++i) {
+      w[m][i] = weight ? value2(rw, i) : two(1.f);
+      b[m][i] = bias ? value2(rb, i) : two(0.f);
     }
   }
 }
 
 // grid (blocks, heads): the CTA's rows are tokens blockIdx.x * rows + i, + gridDim.x * rows, ...
-template <typename T, int MG, int W, int LPR>
+template <typename T, int MG, int W, int LPR, bool FULL>
 __global__ void __launch_bounds__(kThreads, MG == 1 ? 3 : 1)
     msr_affine_kernel(const T* y, const T* g, const float* __restrict__ weight, const float* __restrict__ bias, T* out,
                       int64_t tokens, int heads, int d_v, float eps) {
   constexpr int kRows = kThreads / LPR;
   const int lane = threadIdx.x % LPR, h = blockIdx.y;
-  float w[MG][8], b[MG][8];
+  const float inv_n = 1.f / static_cast<float>(d_v);
+  Two w[MG][4], b[MG][4];
   load_affine<MG, W, LPR>(w, b, weight, bias, h, lane, d_v);
   const int64_t step = static_cast<int64_t>(gridDim.x) * kRows, pitch = static_cast<int64_t>(heads) * d_v;
   const int64_t first = static_cast<int64_t>(blockIdx.x) * kRows;
   int64_t t = first + threadIdx.x / LPR;
   Raw<T> ry[MG], rg[MG];
   auto fetch = [&](int64_t at) {
+    if (at >= tokens) return;
 #pragma unroll
     for (int m = 0; m < MG; ++m) {
       load<W, LPR>(ry[m], y + at * pitch + static_cast<int64_t>(h) * d_v, lane, m, d_v);
       load<W, LPR>(rg[m], g + at * pitch + static_cast<int64_t>(h) * d_v, lane, m, d_v);
     }
   };
-  if (t < tokens) fetch(t);
+  fetch(t);
   for (int64_t t0 = first; t0 < tokens; t0 += step, t += step) {  // all lanes of a warp alike: shuffles
-    float x[MG][8], gv[MG][8];
+    Two x[MG][4], gv[MG][4];
 #pragma unroll
     for (int m = 0; m < MG; ++m)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        x[m][e] = value(ry[m], e);
-        gv[m][e] = value(rg[m], e);
+      for (int i = 0; i < 4; ++i) {
+        x[m][i] = value2(ry[m], i);
+        gv[m][i] = value2(rg[m], i);
       }
-    if (t + step < tokens) fetch(t + step);
-    float mean, inv;
-    row_stats<MG, W, LPR>(x, lane, d_v, eps, mean, inv);
+    fetch(t + step);
+    const Two inv = two(centre<MG, W, LPR, FULL>(x, lane, d_v, inv_n, eps));
     if (t < tokens) {
 #pragma unroll
       for (int m = 0; m < MG; ++m) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          x[m][e] = gv[m][e] * sigmoid(gv[m][e]) * fmaf((x[m][e] - mean) * inv, w[m][e], b[m][e]);
+        for (int i = 0; i < 4; ++i)
+          x[m][i] = mul2(mul2(gv[m][i], sigmoid2(gv[m][i])), fma2(mul2(x[m][i], inv), w[m][i], b[m][i]));
         store<W, LPR>(out + t * pitch + static_cast<int64_t>(h) * d_v, lane, m, d_v, x[m]);
       }
     }
@@ -205,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, MG == 1 ? 3 : 1)
 }
 
 // grid (blocks, heads).  part: [blocks][2][heads][d_v], dw then db.
-template <typename T, int MG, int W, int LPR>
+template <typename T, int MG, int W, int LPR, bool FULL>
 __global__ void __launch_bounds__(kThreads, MG == 1 ? 2 : 1)
     msr_backward_kernel(const T* __restrict__ y, const T* __restrict__ g, const T* __restrict__ dout,
                         const float* __restrict__ weight, const float* __restrict__ bias, T* __restrict__ dy,
@@ -214,17 +240,19 @@ __global__ void __launch_bounds__(kThreads, MG == 1 ? 2 : 1)
   constexpr int kRows = kThreads / LPR;
   const int lane = threadIdx.x % LPR, row = threadIdx.x / LPR, h = blockIdx.y;
   const float inv_n = 1.f / static_cast<float>(d_v);
-  float w[MG][8], b[MG][8], dw[MG][8], db[MG][8];
+  Two w[MG][4], b[MG][4], dw[MG][4], db[MG][4];
   load_affine<MG, W, LPR>(w, b, weight, bias, h, lane, d_v);
 #pragma unroll
   for (int m = 0; m < MG; ++m)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) dw[m][e] = db[m][e] = 0.f;
+    for (int i = 0; i < 4; ++i) dw[m][i] = db[m][i] = two(0.f);
   const int64_t step = static_cast<int64_t>(gridDim.x) * kRows, pitch = static_cast<int64_t>(heads) * d_v;
   const int64_t first = static_cast<int64_t>(blockIdx.x) * kRows;
   int64_t t = first + row;
+  constexpr bool kAhead = MG < 4;  // at MG = 4 the registers are full without the next row
   Raw<T> ry[MG], rg[MG], rd[MG];
   auto fetch = [&](int64_t at) {
+    if (at >= tokens) return;
     at = at * pitch + static_cast<int64_t>(h) * d_v;
 #pragma unroll
     for (int m = 0; m < MG; ++m) {
@@ -233,52 +261,51 @@ __global__ void __launch_bounds__(kThreads, MG == 1 ? 2 : 1)
       load<W, LPR>(rd[m], dout + at, lane, m, d_v);
     }
   };
-  constexpr bool kAhead = MG < 4;  // at MG = 4 the registers are full without the next row
-  if (kAhead && t < tokens) fetch(t);
+  if (kAhead) fetch(t);
   for (int64_t t0 = first; t0 < tokens; t0 += step, t += step) {
-    float x[MG][8], gv[MG][8], d[MG][8];
     const bool live = t < tokens;
-    if (!kAhead && live) fetch(t);
+    if (!kAhead) fetch(t);
+    Two x[MG][4], gv[MG][4], d[MG][4];
 #pragma unroll
     for (int m = 0; m < MG; ++m)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        x[m][e] = value(ry[m], e);
-        gv[m][e] = value(rg[m], e);
-        d[m][e] = value(rd[m], e);
+      for (int i = 0; i < 4; ++i) {
+        x[m][i] = value2(ry[m], i);
+        gv[m][i] = value2(rg[m], i);
+        d[m][i] = value2(rd[m], i);
       }
-    if (kAhead && t + step < tokens) fetch(t + step);
-    float mean, inv;
-    row_stats<MG, W, LPR>(x, lane, d_v, eps, mean, inv);
+    if (kAhead) fetch(t + step);
+    const float inv = centre<MG, W, LPR, FULL>(x, lane, d_v, inv_n, eps);
     const int64_t at = t * pitch + static_cast<int64_t>(h) * d_v;
-    float se = 0.f, sx = 0.f;
+    Two se = two(0.f), sx = two(0.f);
     if (live) {
 #pragma unroll
       for (int m = 0; m < MG; ++m) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float gg = gv[m][e], sg = sigmoid(gg);
-          const float xh = (x[m][e] - mean) * inv;
-          const float n = fmaf(w[m][e], xh, b[m][e]);
-          const float dn = d[m][e] * (gg * sg);
-          gv[m][e] = d[m][e] * n * sg * fmaf(gg, 1.f - sg, 1.f);
-          const float ee = w[m][e] * dn;  // past d_v dout is zero, and so are dn, ee and what they add to
-          db[m][e] += dn;
-          dw[m][e] = fmaf(dn, xh, dw[m][e]);
-          x[m][e] = xh;
-          d[m][e] = ee;
-          se += ee;
-          sx = fmaf(ee, xh, sx);
+        for (int i = 0; i < 4; ++i) {
+          const Two gg = gv[m][i], sg = sigmoid2(gg);
+          const Two xh = mul2(x[m][i], two(inv));
+          const Two n = fma2(w[m][i], xh, b[m][i]);
+          const Two ds = mul2(d[m][i], sg), dn = mul2(ds, gg);
+          // swish'(g) = s (1 + g (1 - s)) = s + g s (1 - s)
+          gv[m][i] = mul2(mul2(ds, n), fma2(gg, fma2(sg, two(-1.f), two(1.f)), two(1.f)));
+          const Two ee = mul2(w[m][i], dn);  // past d_v dout is zero, and so are dn, ee and what they add to
+          db[m][i] = add2(db[m][i], dn);
+          dw[m][i] = fma2(dn, xh, dw[m][i]);
+          x[m][i] = xh;
+          d[m][i] = ee;
+          se = add2(se, ee);
+          sx = fma2(ee, xh, sx);
         }
         store<W, LPR>(dg + at, lane, m, d_v, gv[m]);
       }
     }
-    const float me = row_sum<LPR>(se) * inv_n, mx = row_sum<LPR>(sx) * inv_n;
+    const Two me = two(-row_sum<LPR>(sum_of(se)) * inv_n), mx = two(-row_sum<LPR>(sum_of(sx)) * inv_n);
     if (live) {
 #pragma unroll
       for (int m = 0; m < MG; ++m) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) d[m][e] = inv * (d[m][e] - me - x[m][e] * mx);
+        for (int i = 0; i < 4; ++i) d[m][i] = mul2(two(inv), fma2(x[m][i], mx, add2(d[m][i], me)));
         store<W, LPR>(dy + at, lane, m, d_v, d[m]);
       }
     }
@@ -289,12 +316,15 @@ __global__ void __launch_bounds__(kThreads, MG == 1 ? 2 : 1)
   for (int which = 0; which < 2; ++which) {
     __syncthreads();
 #pragma unroll
-    for (int m = 0; m < MG; ++m)
+    for (int m = 0; m < MG; ++m) {
+      float v[8];
+      spread(which ? db[m] : dw[m], v);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const int c = column<W, LPR>(lane, m, e);
-        if (c < d_v) red[row * d_v + c] = which ? db[m][e] : dw[m][e];
+        if (c < d_v) red[row * d_v + c] = v[e];
       }
+    }
     __syncthreads();
     for (int c = threadIdx.x; c < d_v; c += kThreads) {
       float s = 0.f;
@@ -325,10 +355,11 @@ __global__ void __launch_bounds__(kThreads) msr_reduce_kernel(const float* part,
   }
 }
 
-// CTAs of a head: `per_sm` an SM over all heads, no more than there are rows for.
+// CTAs of a head: `per_sm` an SM over all heads, rounded down (four CTAs in a second wave took the
+// forward from 42 to 60 us), no more than there are rows for.
 int64_t blocks_of(int64_t tokens, int64_t heads, int rows, int per_sm) {
-  const int64_t want = (per_sm * 148 + heads - 1) / heads, most = (tokens + rows - 1) / rows;
-  return want < most ? want : most;
+  const int64_t want = std::max<int64_t>(1, per_sm * 148 / heads);
+  return std::min(want, (tokens + rows - 1) / rows);
 }
 int lanes_per_row(int64_t d_v) { return d_v <= 64 ? 8 : d_v <= 128 ? 16 : 32; }
 int64_t backward_blocks(int64_t tokens, int64_t heads, int64_t d_v) {
@@ -349,10 +380,10 @@ struct Forward {
   const MsrAffineCall& c;
   void* out;
   cudaStream_t s;
-  template <typename T, int MG, int W, int LPR>
+  template <typename T, int MG, int W, int LPR, bool FULL>
   cudaError_t run() {
     const dim3 grid(static_cast<unsigned>(blocks_of(c.tokens, c.heads, kThreads / LPR, 3)), static_cast<unsigned>(c.heads));
-    msr_affine_kernel<T, MG, W, LPR><<<grid, kThreads, 0, s>>>(
+    msr_affine_kernel<T, MG, W, LPR, FULL><<<grid, kThreads, 0, s>>>(
         static_cast<const T*>(c.y), static_cast<const T*>(c.g), c.weight, c.bias, static_cast<T*>(out), c.tokens,
         static_cast<int>(c.heads), static_cast<int>(c.d_v), c.eps);
     return cudaGetLastError();
@@ -365,24 +396,28 @@ struct Backward {
   void* dg;
   float* part;
   cudaStream_t s;
-  template <typename T, int MG, int W, int LPR>
+  template <typename T, int MG, int W, int LPR, bool FULL>
   cudaError_t run() {
     const dim3 grid(static_cast<unsigned>(backward_blocks(c.tokens, c.heads, c.d_v)), static_cast<unsigned>(c.heads));
     // at most 32 KB: kThreads / LPR rows of at most 8 LPR (LPR < 32) or 1024 values
     const size_t smem = part ? sizeof(float) * (kThreads / LPR) * static_cast<size_t>(c.d_v) : 0;
-    msr_backward_kernel<T, MG, W, LPR><<<grid, kThreads, smem, s>>>(
+    msr_backward_kernel<T, MG, W, LPR, FULL><<<grid, kThreads, smem, s>>>(
         static_cast<const T*>(c.y), static_cast<const T*>(c.g), static_cast<const T*>(dout), c.weight, c.bias,
         static_cast<T*>(dy), static_cast<T*>(dg), part, c.tokens, static_cast<int>(c.heads), static_cast<int>(c.d_v), c.eps);
     return cudaGetLastError();
   }
 };
+template <typename T, int W, int MG, int LPR, typename F>
+cudaError_t by_fullness(int64_t d_v, F& f) {
+  return d_v == 8 * MG * LPR ? f.template run<T, MG, W, LPR, true>() : f.template run<T, MG, W, LPR, false>();
+}
 template <typename T, int W, typename F>
 cudaError_t by_row(int64_t d_v, F& f) {
-  if (d_v <= 64) return f.template run<T, 1, W, 8>();
-  if (d_v <= 128) return f.template run<T, 1, W, 16>();
-  if (d_v <= 256) return f.template run<T, 1, W, 32>();
-  if (d_v <= 512) return f.template run<T, 2, W, 32>();
-  return f.template run<T, 4, W, 32>();
+  if (d_v <= 64) return by_fullness<T, W, 1, 8>(d_v, f);
+  if (d_v <= 128) return by_fullness<T, W, 1, 16>(d_v, f);
+  if (d_v <= 256) return by_fullness<T, W, 1, 32>(d_v, f);
+  if (d_v <= 512) return by_fullness<T, W, 2, 32>(d_v, f);
+  return by_fullness<T, W, 4, 32>(d_v, f);
 }
 template <typename F>
 cudaError_t dispatch(const MsrAffineCall& c, F& f, const void* p0, const void* p1, const void* p2) {

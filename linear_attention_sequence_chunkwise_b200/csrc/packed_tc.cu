@@ -14,6 +14,7 @@
 // factor instead of one a pair; gamma^128 >= 2^-12 keeps both in fp16's normal range.  The masked
 // scores stay in tensor memory as two bf16 numbers (2^-17), so that v is read as it is.  Each
 // rounding outside fp16's range is counted (retnet_fp16_range_errors).
+#include "fp32x2.cuh"
 #include "packed.cuh"
 #include "pdl.cuh"
 #include "sm100_ptx.cuh"
@@ -51,30 +52,6 @@ struct TcPackedArgs {
 __device__ __forceinline__ int64_t blocked(int row, int col, int d_k) {
   return (static_cast<int64_t>(col / 8) * d_k + row) * 8 + col % 8;
 }
-
-// Pairs of floats for the packed fp32 instructions (two lanes an instruction).
-using Two = uint64_t;
-__device__ __forceinline__ Two two(float a, float b) {
-  Two r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float2 parts(Two x) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
-  return r;
-}
-__device__ __forceinline__ Two mul2(Two a, Two b) {
-  Two r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
-  Two r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ Two neg2(Two a) { return a ^ 0x8000000080000000ull; }
 
 // Cosines and sines of four pairs, two and two.
 struct Turn {

@@ -534,9 +534,9 @@ retnet_status_t retnet_msr_epilogue(const void* y, const void* g, void* out, int
 namespace {
 bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-size_t packed_workspace_bytes(int64_t rows, int64_t seqs, int64_t heads_kv, int64_t d_k, int64_t d_v) {
-  return std::max(packed_simt_workspace_bytes(rows, seqs, heads_kv, d_k, d_v),
-                  packed_tc_workspace_bytes(rows, seqs, heads_kv, d_k, d_v));
+size_t packed_workspace_bytes(const retnet_packed_t& d) {
+  return std::max(packed_simt_workspace_bytes(d.tokens, d.seqs, d.heads, d.heads_kv, d.d_k, d.d_v),
+                  packed_tc_workspace_bytes(d.tokens, d.seqs, d.heads_kv, d.d_k, d.d_v));
 }
 
 // What the packed call and its single-token form check alike; seqs: entries of slots and pos.
@@ -572,8 +572,9 @@ PackedCall packed_call(const void* q, const void* k, const void* v, void* o, con
 
 retnet_status_t retnet_packed_workspace_size(retnet_packed_t dims, size_t* bytes) {
   if (!bytes) return RETNET_ERR_NULL_PTR;
-  if (dims.tokens < 0 || dims.seqs < 0 || dims.heads_kv < 0 || dims.d_k < 0 || dims.d_v < 0) return RETNET_ERR_BAD_SHAPE;
-  *bytes = packed_workspace_bytes(dims.tokens, dims.seqs, dims.heads_kv, dims.d_k, dims.d_v);
+  if (dims.tokens < 0 || dims.seqs < 0 || dims.heads <= 0 || dims.heads_kv <= 0 || dims.d_k <= 0 || dims.d_v <= 0)
+    return RETNET_ERR_BAD_SHAPE;
+  *bytes = packed_workspace_bytes(dims);
   return RETNET_OK;
 }
 
@@ -590,7 +591,7 @@ retnet_status_t retnet_retention_packed(const void* q, const void* k, const void
   if ((st = check_packed_pointers(c)) != RETNET_OK) return st;
   if (!cu_seqlens || !workspace) return RETNET_ERR_NULL_PTR;
   if (!aligned_to(cu_seqlens, 4) || !aligned16(workspace) ||
-      workspace_bytes < packed_workspace_bytes(c.rows, c.seqs, c.heads_kv, c.d_k, c.d_v))
+      workspace_bytes < packed_workspace_bytes(dims))
     return RETNET_ERR_BAD_PARAM;
   if ((st = check_device()) != RETNET_OK) return st;
   c.ws = workspace;

@@ -193,7 +193,7 @@ def test_bitwise_repeatable_and_on_its_stream():
         def eager(lens, sl, ps):
             return run(fused, pool, lens, sl, ps, gamma, theta, hq, kv, dk, dv)
         want_a, want_b = eager(lens_a, slots, pos), eager(lens_b, slots[::-1], pos[::-1])
-        ws = torch.full((rn.retnet_packed_workspace_size((rows, 3, kv, dk, dv)),), 255, dtype=torch.uint8, device="cuda")
+        ws = torch.full((rn.retnet_packed_workspace_size((rows, 3, hq, kv, dk, dv)),), 255, dtype=torch.uint8, device="cuda")
         side = torch.cuda.Stream()
         side.wait_stream(torch.cuda.current_stream())
         got = run(fused, pool, lens_a, slots, pos, gamma, theta, hq, kv, dk, dv, stream=side, workspace=ws)

@@ -70,7 +70,7 @@ def test_packed_refusals(lib):
     assert _packed(lib, q=FAKE + 2) == 4 and _packed(lib, q=FAKE + 1, dtype=1) == 4
     assert _packed(lib, cu=FAKE + 2) == 4 and _packed(lib, slots=FAKE + 2) == 4 and _packed(lib, pos=FAKE + 4) == 4
     assert _packed(lib, pool=FAKE + 4) == 4 and _packed(lib, ws=FAKE + 8) == 4
-    n = rn.retnet_packed_workspace_size((10, 2, 2, 16, 8))
+    n = rn.retnet_packed_workspace_size((10, 2, 4, 2, 16, 8))
     assert n > 0 and _packed(lib, ws_bytes=n - 1) == 4
     assert _packed(lib, _dims(tokens=0), q=None) == 0 and _packed(lib, _dims(seqs=0), cu=None) == 0  # no work
 
