@@ -186,7 +186,7 @@ __device__ __forceinline__ void load_affine(Two (&w)[MG][4], Two (&b)[MG][4], co
 
 // grid (blocks, heads): the CTA's rows are tokens blockIdx.x * rows + i, + gridDim.x * rows, ...
 template <typename T, int MG, int W, int LPR, bool FULL>
-__global__ void __launch_bounds__(kThreads, MG == 1 ? 3 : 1)
+__global__ void __launch_bounds__(kThreads, MG == 1 ? 4 : 1)
     msr_affine_kernel(const T* y, const T* g, const float* __restrict__ weight, const float* __restrict__ bias, T* out,
                       int64_t tokens, int heads, int d_v, float eps) {
   constexpr int kRows = kThreads / LPR;
@@ -382,7 +382,7 @@ struct Forward {
   cudaStream_t s;
   template <typename T, int MG, int W, int LPR, bool FULL>
   cudaError_t run() {
-    const dim3 grid(static_cast<unsigned>(blocks_of(c.tokens, c.heads, kThreads / LPR, 3)), static_cast<unsigned>(c.heads));
+    const dim3 grid(static_cast<unsigned>(blocks_of(c.tokens, c.heads, kThreads / LPR, 4)), static_cast<unsigned>(c.heads));
     msr_affine_kernel<T, MG, W, LPR, FULL><<<grid, kThreads, 0, s>>>(
         static_cast<const T*>(c.y), static_cast<const T*>(c.g), c.weight, c.bias, static_cast<T*>(out), c.tokens,
         static_cast<int>(c.heads), static_cast<int>(c.d_v), c.eps);

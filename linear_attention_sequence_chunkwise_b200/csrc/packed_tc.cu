@@ -161,6 +161,7 @@ __device__ __forceinline__ void report(const __half2& mx) {
 // it is kept to the 8 steps that one plane takes.  Two CTAs an SM cover one another's waits.
 template <int M, int NV>
 struct StateCfg {
+  static constexpr int kThreads = M == 128 ? 512 : 256;
   static constexpr int kStep = 64;
   static constexpr int kPlane = kStep * M * 2, kVBytes = kStep * NV * 2;
   static constexpr int kSmem = 4 * kPlane + 2 * kVBytes + 1024;  // raw / first planes x 2, second, third, v x 2
@@ -168,7 +169,7 @@ struct StateCfg {
 };
 
 template <int M, int NV>
-__global__ void __launch_bounds__(256, 2) tc_state_kernel(TcPackedArgs a, HeadParams hp) {
+__global__ void __launch_bounds__(StateCfg<M, NV>::kThreads, 2) tc_state_kernel(TcPackedArgs a, HeadParams hp) {
   using C = StateCfg<M, NV>;
   extern __shared__ unsigned char raw_smem[];
   __shared__ uint64_t bar;
@@ -182,27 +183,30 @@ __global__ void __launch_bounds__(256, 2) tc_state_kernel(TcPackedArgs a, HeadPa
   const int k0 = (blockIdx.z / slices) * M, v0 = (blockIdx.z % slices) * NV;
   const uint32_t sm = (smem_addr(raw_smem) + 1023u) & ~1023u, s2 = sm + 2 * C::kPlane, sv = sm + 4 * C::kPlane,
                  b = smem_addr(&bar);
-  constexpr int kGroups = M / 8, kRows = 256 / kGroups, kPer = C::kStep / kRows;  // rows at once, rows a thread
+  constexpr int kGroups = M / 8, kRows = C::kThreads / kGroups, kPer = C::kStep / kRows;  // rows at once, rows a thread
   const int g = tid % kGroups, tr = tid / kGroups;
   const __nv_bfloat16* kp = a.k + static_cast<int64_t>(d.row) * a.stride_k + static_cast<int64_t>(h) * a.d_k + k0 + g * 8;
   const __nv_bfloat16* vp = a.v + static_cast<int64_t>(d.row) * a.stride_v + static_cast<int64_t>(h) * a.d_v + v0;
   const int steps = d.tokens > C::kStep ? 2 : 1;
-  const uint32_t mine = (g / 8) * (C::kStep * 128);  // this thread's column block
+  const uint32_t mine = (g / 8) * (C::kStep * 128) + sw128(tr, g % 8);  // kRows more rows: kRows * 128 bytes on
+  constexpr int kVPer = C::kStep * (NV / 8) / C::kThreads, kVRows = C::kThreads / (NV / 8);
+  static_assert(kVRows % 8 == 0 && kRows % 16 == 0, "rows kVRows apart are swizzled alike; a thread's rows share t % 16");
+  const int vr = tid / (NV / 8), vc = tid % (NV / 8);
+  const uint32_t v_mine = (vc / 8) * (C::kStep * 128) + sw128(vr, vc % 8);
 #pragma unroll
   for (int st = 0; st < 2; ++st) {
     if (st < steps) {
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        const int r = tr + i * kRows, t = st * C::kStep + r;
+        const int t = st * C::kStep + tr + i * kRows;
         const bool in = t < d.tokens;
-        cp_async16(sm + st * C::kPlane + mine + sw128(r, g % 8), kp + static_cast<int64_t>(in ? t : 0) * a.stride_k, in);
+        cp_async16(sm + st * C::kPlane + mine + i * kRows * 128, kp + static_cast<int64_t>(in ? t : 0) * a.stride_k, in);
       }
 #pragma unroll
-      for (int e = tid; e < C::kStep * (NV / 8); e += 256) {
-        const int r = e / (NV / 8), c = e % (NV / 8), t = st * C::kStep + r;
+      for (int i = 0; i < kVPer; ++i) {
+        const int t = st * C::kStep + vr + i * kVRows;
         const bool in = t < d.tokens;
-        cp_async16(sv + st * C::kVBytes + (c / 8) * (C::kStep * 128) + sw128(r, c % 8),
-                   vp + static_cast<int64_t>(in ? t : 0) * a.stride_v + c * 8, in);
+        cp_async16(sv + st * C::kVBytes + v_mine + i * kVRows * 128, vp + static_cast<int64_t>(in ? t : 0) * a.stride_v + vc * 8, in);
       }
     }
     cp_async_commit();
@@ -234,14 +238,14 @@ __global__ void __launch_bounds__(256, 2) tc_state_kernel(TcPackedArgs a, HeadPa
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int r = tr + i * kRows, at = (st * C::kStep + r) / 16;
-      const uint32_t to = sm + st * C::kPlane + mine + sw128(r, g % 8);
+      const uint32_t to = sm + st * C::kPlane + mine + i * kRows * 128;
       y[i] = turned(ld_shared_u4(to), product(scaled(load_turn(base + at * a.d_k), decay_pow(lg, 112 - 16 * at)), off));
       store_plane(to, y[i]);
     }
     if (st == 1) dead = !mbar_wait(b, 0, kDrainBudget);  // the first step's products have read planes 2 and 3
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const uint32_t to = s2 + mine + sw128(tr + i * kRows, g % 8);
+      const uint32_t to = s2 + mine + i * kRows * 128;
       store_plane(to, y[i]);
       store_plane(to + C::kPlane, y[i]);
     }
@@ -272,7 +276,7 @@ __global__ void __launch_bounds__(256, 2) tc_state_kernel(TcPackedArgs a, HeadPa
     const uint32_t lanes = tm + (static_cast<uint32_t>(quarter * 32) << 16);
     float* w = a.w + (static_cast<int64_t>(blockIdx.x) * a.kv + h) * a.d_k * a.d_v;
 #pragma unroll
-    for (int c = (warp / 4) * 32; c < NV; c += 64) {
+    for (int c = (warp / 4) * 32; c < NV; c += C::kThreads / 4) {
       uint32_t r[2][16];
       tmem_ld_wait(lanes + c, r);
       if (M == 128 || lane < 16) {
@@ -876,8 +880,8 @@ cudaError_t launch_chunks(const PackedCall& c, const TcPackedArgs& a, const Head
   if (e != cudaSuccess) return e;
   const unsigned kv = static_cast<unsigned>(a.kv);
   e = launch_dependent(tc_state_kernel<M, NV>,
-                       dim3(static_cast<unsigned>(a.units), kv, static_cast<unsigned>((a.d_k / M) * (a.d_v / NV))), dim3(256),
-                       C::kSmem, s, a, hp);
+                       dim3(static_cast<unsigned>(a.units), kv, static_cast<unsigned>((a.d_k / M) * (a.d_v / NV))),
+                       dim3(C::kThreads), C::kSmem, s, a, hp);
   if (e != cudaSuccess) return e;
   const unsigned nb = static_cast<unsigned>((static_cast<int64_t>(a.d_k) * a.d_v / 4 + kScanThreads - 1) / kScanThreads);
   return launch_dependent(tc_scan_kernel, dim3(nb, kv, static_cast<unsigned>(c.seqs)), dim3(kScanThreads), 0, s, a, hp);

@@ -5,18 +5,20 @@
 //
 // Bound by HBM: each pair reads and writes one slot.  "All sources before any destination" needs no
 // second copy of the pool when one CTA moves the SAME columns of every pair: a CTA owns a tile of
-// `cols` floats of the slot, reads it for all pairs, then writes it for all pairs; tiles do not
-// touch one another.  Only where some pair's source is another pair's destination does the read have
-// to be complete before the first write (the tile is staged in shared memory, kStageBytes for all
-// pairs); otherwise the tile streams through registers.
+// `cols` columns (16 bytes each) of the slot, reads it for all pairs, then writes it for all pairs;
+// tiles do not touch one another.  Only where some pair's source is another pair's destination does
+// the read have to be complete before the first write: the tile is staged in shared memory by
+// asynchronous copies, 64 KB at once, two CTAs an SM, one storing while the other loads.  Otherwise it
+// streams through registers.
 #include "launch.h"
+#include "sm100_ptx.cuh"
 
 namespace retnet {
 namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxPairs = RETNET_MAX_SLOT_PAIRS;
-constexpr int kStageBytes = 64 * 1024;  // three CTAs an SM
+constexpr int kStageBytes = 64 * 1024;
 constexpr int kUnroll = 8;
 
 __device__ unsigned int g_slot_errors = 0;
@@ -28,9 +30,10 @@ __device__ __forceinline__ float zero_of<float>() { return 0.f; }
 template <>
 __device__ __forceinline__ float4 zero_of<float4>() { return make_float4(0.f, 0.f, 0.f, 0.f); }
 
-// T: float4, or float where a slot is no multiple of four floats.  n_cols, cols in units of T.
+// T: float4, or float where a slot is no multiple of four floats.  n_cols, cols in units of T; cols a
+// power of two.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) slots_copy_kernel(T* pool, int32_t n_slots, int64_t n_cols, int cols,
+__global__ void __launch_bounds__(kThreads) slots_copy_kernel(T* pool, int32_t n_slots, int64_t n_cols, int log_cols,
                                                               const int32_t* __restrict__ src,
                                                               const int32_t* __restrict__ dst, int n) {
   extern __shared__ __align__(16) unsigned char stage_raw[];
@@ -67,41 +70,49 @@ __global__ void __launch_bounds__(kThreads) slots_copy_kernel(T* pool, int32_t n
   }
   const bool hazard = __syncthreads_or(mine) != 0;
 
+  // element e of the tile: column e % cols of pair e / cols
+  const int cols = 1 << log_cols, total = m << log_cols;
   for (int64_t c0 = static_cast<int64_t>(blockIdx.x) * cols; c0 < n_cols; c0 += static_cast<int64_t>(gridDim.x) * cols) {
     const int w = static_cast<int>(n_cols - c0 < cols ? n_cols - c0 : cols);
-    const int total = m * w;
+    T* at = pool + c0;
+    if (hazard) {
+      for (int e = tid; e < total; e += kThreads) {
+        const int c = e & (cols - 1);
+        const int32_t s = sp[e >> log_cols];
+        if (c >= w) continue;
+        if (s < 0) {
+          stage[e] = zero_of<T>();
+        } else if constexpr (sizeof(T) == 16) {
+          sm100::cp_async16(sm100::smem_addr(stage + e), at + static_cast<int64_t>(s) * n_cols + c, true);
+        } else {
+          stage[e] = at[static_cast<int64_t>(s) * n_cols + c];
+        }
+      }
+      sm100::cp_async_wait_all();
+      __syncthreads();
+      for (int e = tid; e < total; e += kThreads) {
+        const int c = e & (cols - 1);
+        if (c < w) at[static_cast<int64_t>(dp[e >> log_cols]) * n_cols + c] = stage[e];
+      }
+      __syncthreads();
+      continue;
+    }
     for (int e0 = tid; e0 < total; e0 += kThreads * kUnroll) {
       T x[kUnroll];
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
-        const int e = e0 + u * kThreads;
+        const int e = e0 + u * kThreads, c = e & (cols - 1);
         x[u] = zero_of<T>();
-        if (e < total) {
-          const int i = e / w;
-          const int32_t s = sp[i];
-          if (s >= 0) x[u] = pool[static_cast<int64_t>(s) * n_cols + c0 + (e - i * w)];
+        if (e < total && c < w) {
+          const int32_t s = sp[e >> log_cols];
+          if (s >= 0) x[u] = at[static_cast<int64_t>(s) * n_cols + c];
         }
       }
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
-        const int e = e0 + u * kThreads;
-        if (e < total) {
-          if (hazard) {
-            stage[e] = x[u];
-          } else {
-            const int i = e / w;
-            pool[static_cast<int64_t>(dp[i]) * n_cols + c0 + (e - i * w)] = x[u];
-          }
-        }
+        const int e = e0 + u * kThreads, c = e & (cols - 1);
+        if (e < total && c < w) at[static_cast<int64_t>(dp[e >> log_cols]) * n_cols + c] = x[u];
       }
-    }
-    if (hazard) {
-      __syncthreads();
-      for (int e = tid; e < total; e += kThreads) {
-        const int i = e / w;
-        pool[static_cast<int64_t>(dp[i]) * n_cols + c0 + (e - i * w)] = stage[e];
-      }
-      __syncthreads();
     }
   }
 }
@@ -110,19 +121,20 @@ template <typename T>
 cudaError_t launch_typed(float* pool, int64_t slots, int64_t slot_floats, const int32_t* src, const int32_t* dst,
                          int64_t n, cudaStream_t s) {
   const int64_t n_cols = slot_floats * static_cast<int64_t>(sizeof(float)) / static_cast<int64_t>(sizeof(T));
-  int cols = kStageBytes / static_cast<int>(sizeof(T)) / static_cast<int>(n);
-  if (cols >= 32) cols -= cols % 32;
-  if (cols > n_cols) cols = static_cast<int>(n_cols);
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(slots_copy_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStageBytes);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = (n_cols + cols - 1) / cols;
+  // The widest power of two that the stage has room for (n <= 1024: at least 64 bytes), but no wider
+  // than leaves two tiles an SM: four pairs of 512 KB slots took 8 us in 32 tiles.
+  int log_cols = 0;
+  while (static_cast<size_t>(2 << log_cols) * sizeof(T) * n <= kStageBytes && (n_cols >> (log_cols + 1)) >= 2 * sms) ++log_cols;
+  const int64_t tiles = (n_cols + (1 << log_cols) - 1) >> log_cols;
   const int64_t blocks = tiles < 2 * sms ? tiles : 2 * sms;
-  slots_copy_kernel<T><<<static_cast<unsigned>(blocks), kThreads, static_cast<size_t>(cols) * n * sizeof(T), s>>>(
-      reinterpret_cast<T*>(pool), static_cast<int32_t>(slots), n_cols, cols, src, dst, static_cast<int>(n));
+  slots_copy_kernel<T><<<static_cast<unsigned>(blocks), kThreads, (static_cast<size_t>(n) << log_cols) * sizeof(T), s>>>(
+      reinterpret_cast<T*>(pool), static_cast<int32_t>(slots), n_cols, log_cols, src, dst, static_cast<int>(n));
   return cudaGetLastError();
 }
 
