@@ -33,7 +33,8 @@ __device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
-__device__ __forceinline__ Two neg2(Two a) { return a ^ 0x8000000080000000ull; }
+// (by the FMA units: two sign flips would be two instructions of the integer pipe)
+__device__ __forceinline__ Two neg2(Two a) { return mul2(a, 0xbf800000bf800000ull); }
 __device__ __forceinline__ float sum_of(Two a) {
   const float2 p = parts(a);
   return p.x + p.y;

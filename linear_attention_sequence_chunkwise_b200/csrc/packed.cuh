@@ -36,8 +36,9 @@ inline int64_t packed_units(int64_t rows, int64_t seqs, int64_t run) { return ro
 
 // The rotation of a token is base x offset (complex products): base[unit][i] turns the pairs by the
 // angle of the run's token 16 i, offset[r] by that of r further tokens, so that a kernel needs no sine
-// or cosine of its own.  base: [units][run / 16][2 half] floats, offset: [17][2 half]; nullptr: not
-// written.  A row holds, for every four pairs, their cosines and then their sines.
+// or cosine of its own.  base: [units][blocks of up to 128 columns][run / 16][columns] floats, offset:
+// [17][2 half]; nullptr: not written.  A row holds, for every four pairs, their cosines and then their
+// sines.
 struct PackedRotation {
   float* base;
   float* offset;

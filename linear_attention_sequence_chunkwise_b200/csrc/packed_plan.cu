@@ -11,12 +11,12 @@ constexpr int kThreads = 512;
 
 __device__ unsigned int g_packed_errors = 0;
 
-// Rotation of pair j by position p, into its places in a row.
+// Rotation of pair j by position p, into its places: row[0] its cosine, row[4] its sine.
 __device__ __forceinline__ void turn(float* row, const PackedRotation& rot, int64_t p, int j, const HeadParams& hp) {
   float s = 0.f, c = 1.f;
   if (rot.xpos) position_sincos(p, hp.theta[j], &s, &c);
-  row[j / 4 * 8 + j % 4] = c;
-  row[j / 4 * 8 + 4 + j % 4] = s;
+  row[0] = c;
+  row[4] = s;
 }
 
 // One CTA a unit.  The sequence of a unit is the last one whose first unit is not behind it.  A call
@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PackedIndex ix, RunDesc*
   bad = __syncthreads_or(bad);
   if (rot.offset)  // its rows dealt out to the CTAs
     for (int64_t r = u; r < 17; r += gridDim.x)
-      for (int j = tid; j < rot.half; j += kThreads) turn(rot.offset + r * 2 * rot.half, rot, r, j, hp);
+      for (int j = tid; j < rot.half; j += kThreads) turn(rot.offset + r * 2 * rot.half + j / 4 * 8 + j % 4, rot, r, j, hp);
   const int s = total - 1;  // -1: the first sequence starts behind this unit
   if (bad || s < 0) {
     if (tid == 0) {
@@ -82,9 +82,12 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PackedIndex ix, RunDesc*
                    : RunDesc{0, 0, 0, 0, 0, 0, 0};
   }
   if (!rot.base || !live) return;
-  const int rows = ix.run / 16;
-  for (int e = tid; e < rows * rot.half; e += kThreads)
-    turn(rot.base + (u * rows + e / rot.half) * 2 * rot.half, rot, pos + i * ix.run + 16 * (e / rot.half), e % rot.half, hp);
+  const int rows = ix.run / 16, width = 2 * rot.half < 128 ? 2 * rot.half : 128;
+  for (int e = tid; e < rows * rot.half; e += kThreads) {
+    const int r = e / rot.half, j = e % rot.half, col = j / 4 * 8 + j % 4;
+    turn(rot.base + (u * rot.half * 2 + col / width * width) * rows + r * width + col % width, rot,
+         pos + i * ix.run + 16 * r, j, hp);
+  }
 }
 
 }  // namespace

@@ -14,6 +14,8 @@
 // factor instead of one a pair; gamma^128 >= 2^-12 keeps both in fp16's normal range.  The masked
 // scores stay in tensor memory as two bf16 numbers (2^-17), so that v is read as it is.  Each
 // rounding outside fp16's range is counted (retnet_fp16_range_errors).
+#include <algorithm>
+
 #include "fp32x2.cuh"
 #include "packed.cuh"
 #include "pdl.cuh"
@@ -35,7 +37,7 @@ struct TcPackedArgs {
   __nv_bfloat16* o;
   float* pool;
   const RunDesc* desc;
-  const float* base;    // [units][8][d_k], rotations (packed.cuh)
+  const float* base;    // [units][d_k / M][8][M], M = min(d_k, 128): rotations (packed.cuh)
   const float* offset;  // [17][d_k]
   float* w;             // [units][heads_kv] states of chunks, in blocks of eight columns (below)
   __half* r16;          // [units][heads_kv] states before the chunks, the same
@@ -112,7 +114,7 @@ __device__ __forceinline__ float rest(float x) { return x - __uint_as_float(__fl
 // x less its truncation to bf16, both lanes (exact).
 __device__ __forceinline__ Two rest2(Two x) { return fma2(x & 0xffff0000ffff0000ull, 0xbf800000bf800000ull, x); }
 // The bf16 plane of y (truncated) to shared memory; y keeps what is left.
-__device__ __forceinline__ void store_plane(uint32_t to, Eight& y) {
+__device__ __forceinline__ void store_plane(unsigned char* to, Eight& y) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -122,12 +124,7 @@ __device__ __forceinline__ void store_plane(uint32_t to, Eight& y) {
     y.first[i] = rest2(y.first[i]);
     y.second[i] = rest2(y.second[i]);
   }
-  st_shared_v4(to, w[0], w[1], w[2], w[3]);
-}
-__device__ __forceinline__ uint4 ld_shared_u4(uint32_t at) {
-  uint4 x;
-  ld_shared_v4(at, x.x, x.y, x.z, x.w);
-  return x;
+  *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 // gamma^n - 1 to full relative precision: a state decayed by fma(that, S, S) keeps the factor's
 // accuracy where the factor itself, near 1, would round the same way chunk after chunk.
@@ -144,206 +141,90 @@ __device__ __forceinline__ float row_factor32(float gamma, int d_k, int64_t p, u
   return f;
 }
 
-// fp16 range check of packed pairs: the largest magnitude so far, NaN kept.
-__device__ __forceinline__ void track(__half2& mx, uint32_t w) {
-  mx = __hmax2_nan(mx, __habs2(*reinterpret_cast<const __half2*>(&w)));
-}
-__device__ __forceinline__ void report(const __half2& mx) {
-  const float2 f = __half22float2(mx);
-  report_fp16_range(fmaxf(f.x, f.y) + (f.x - f.x) + (f.y - f.y));
+// Largest magnitude so far (NaN kept), for the fp16 range report.
+__device__ __forceinline__ void track(float& mx, float a, float b) {
+  asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(mx) : "f"(a), "f"(b));
 }
 
-// ---- state: W of one chunk -------------------------------------------------------------------
-// CTA = (chunk, key/value head, up to 128 rows of d_k x NV columns of d_v).  All of the chunk's k and v
-// is fetched at once by asynchronous copies; k is rotated and cut in two steps of 64 tokens, its first
-// plane written over the raw rows.  The first planes' products and the other two's go to
-// accumulators of their own: a tensor-core sum drops what lies below its running value's last bit, so
-// it is kept to the 8 steps that one plane takes.  Two CTAs an SM cover one another's waits.
+// ---- states ----------------------------------------------------------------------------------
+// One kernel, two walks.  A CTA holds up to 128 rows of d_k x NV columns of d_v and takes chunks in turn:
+//   SEQ   the chunks of one (sequence, key/value head) in order: the fp32 state in registers (at most
+//         64 values a thread); before each chunk its fp16 rounding goes to r16, after the last the
+//         state goes to the pool.  No W, no scan.
+//   else  every chunk of every head, dealt out to one CTA an SM: the products W of a chunk to memory.
+// Chunks run in steps of 64 tokens through a ring of three: one warp fetches (TMA: k, v, and the step's
+// rotations), the data warps rotate k and cut it into planes in place and, behind a chunk's last step,
+// take the products of the chunk before out of one of two accumulators, one warp issues the products.
+// A data warp that also issued them held the others up for as long as they ran, and one CTA a chunk
+// spent a third of its 7 us on starting (32 us a call of 768 chunk-heads of 128 x 128).
 template <int M, int NV>
 struct StateCfg {
-  static constexpr int kThreads = M == 128 ? 512 : 256;
-  static constexpr int kStep = 64;
-  static constexpr int kPlane = kStep * M * 2, kVBytes = kStep * NV * 2;
-  static constexpr int kSmem = 4 * kPlane + 2 * kVBytes + 1024;  // raw / first planes x 2, second, third, v x 2
-  static constexpr int kCols = NV;
-};
-
-template <int M, int NV>
-__global__ void __launch_bounds__(StateCfg<M, NV>::kThreads, 2) tc_state_kernel(TcPackedArgs a, HeadParams hp) {
-  using C = StateCfg<M, NV>;
-  extern __shared__ unsigned char raw_smem[];
-  __shared__ uint64_t bar;
-  __shared__ uint32_t tmem_at;
-  pdl_wait();
-  pdl_go();
-  const RunDesc d = a.desc[blockIdx.x];
-  if (d.tokens == 0) return;
-  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  const int h = blockIdx.y, slices = a.d_v / NV;
-  const int k0 = (blockIdx.z / slices) * M, v0 = (blockIdx.z % slices) * NV;
-  const uint32_t sm = (smem_addr(raw_smem) + 1023u) & ~1023u, s2 = sm + 2 * C::kPlane, sv = sm + 4 * C::kPlane,
-                 b = smem_addr(&bar);
-  constexpr int kGroups = M / 8, kRows = C::kThreads / kGroups, kPer = C::kStep / kRows;  // rows at once, rows a thread
-  const int g = tid % kGroups, tr = tid / kGroups;
-  const __nv_bfloat16* kp = a.k + static_cast<int64_t>(d.row) * a.stride_k + static_cast<int64_t>(h) * a.d_k + k0 + g * 8;
-  const __nv_bfloat16* vp = a.v + static_cast<int64_t>(d.row) * a.stride_v + static_cast<int64_t>(h) * a.d_v + v0;
-  const int steps = d.tokens > C::kStep ? 2 : 1;
-  const uint32_t mine = (g / 8) * (C::kStep * 128) + sw128(tr, g % 8);  // kRows more rows: kRows * 128 bytes on
-  constexpr int kVPer = C::kStep * (NV / 8) / C::kThreads, kVRows = C::kThreads / (NV / 8);
-  static_assert(kVRows % 8 == 0 && kRows % 16 == 0, "rows kVRows apart are swizzled alike; a thread's rows share t % 16");
-  const int vr = tid / (NV / 8), vc = tid % (NV / 8);
-  const uint32_t v_mine = (vc / 8) * (C::kStep * 128) + sw128(vr, vc % 8);
-#pragma unroll
-  for (int st = 0; st < 2; ++st) {
-    if (st < steps) {
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int t = st * C::kStep + tr + i * kRows;
-        const bool in = t < d.tokens;
-        cp_async16(sm + st * C::kPlane + mine + i * kRows * 128, kp + static_cast<int64_t>(in ? t : 0) * a.stride_k, in);
-      }
-#pragma unroll
-      for (int i = 0; i < kVPer; ++i) {
-        const int t = st * C::kStep + vr + i * kVRows;
-        const bool in = t < d.tokens;
-        cp_async16(sv + st * C::kVBytes + v_mine + i * kVRows * 128, vp + static_cast<int64_t>(in ? t : 0) * a.stride_v + vc * 8, in);
-      }
-    }
-    cp_async_commit();
-  }
-  if (warp == 0) {
-    tmem_alloc(smem_addr(&tmem_at), C::kCols);
-    tmem_relinquish();  // or the SM's next CTA waits for this one's end
-  }
-  if (tid == 0) {
-    mbar_init(b, 1);
-    fence_mbar_init();
-  }
-  const float lg = hp.log2g[h];
-  // the decay to the chunk's end, gamma^(127-t) = gamma^(112-16i) gamma^(15-r), t = 16 i + r
-  const Turn off = scaled(load_turn(a.offset + (tr % 16) * a.d_k + k0 + g * 8), decay_pow(lg, 15 - tr % 16));
-  const float* base = a.base + static_cast<int64_t>(blockIdx.x) * 8 * a.d_k + k0 + g * 8;
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tm = tmem_at;
-  constexpr uint32_t ID = idesc_bf16_f32(M, NV, 1, 1);
-  bool dead = false;
-#pragma unroll
-  for (int st = 0; st < 2; ++st) {
-    if (st >= steps) break;
-    if (st == 0) cp_async_wait<1>();
-    else cp_async_wait<0>();
-    Eight y[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int r = tr + i * kRows, at = (st * C::kStep + r) / 16;
-      const uint32_t to = sm + st * C::kPlane + mine + i * kRows * 128;
-      y[i] = turned(ld_shared_u4(to), product(scaled(load_turn(base + at * a.d_k), decay_pow(lg, 112 - 16 * at)), off));
-      store_plane(to, y[i]);
-    }
-    if (st == 1) dead = !mbar_wait(b, 0, kDrainBudget);  // the first step's products have read planes 2 and 3
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const uint32_t to = s2 + mine + i * kRows * 128;
-      store_plane(to, y[i]);
-      store_plane(to + C::kPlane, y[i]);
-    }
-    fence_proxy_async_smem();
-    if (__syncthreads_or(dead)) {
-      dead = true;
-      break;
-    }
-    if (tid == 0) {
-      const uint64_t dv = sdesc_sw128(sv + st * C::kVBytes, C::kStep * 128, 1024);
-#pragma unroll
-      for (int p = 2; p >= 0; --p) {
-        const uint64_t dk = sdesc_sw128(p == 0 ? sm + st * C::kPlane : s2 + (p - 1) * C::kPlane, C::kStep * 128, 1024);
-#pragma unroll
-        for (int ks = 0; ks < C::kStep / 16; ++ks)
-          mma_f16_ss(tm, dk + ((ks * 2048) >> 4), dv + ((ks * 2048) >> 4), ID, st > 0 || p < 2 || ks > 0);
-      }
-      mma_commit(b);
-    }
-  }
-  if (!dead) dead = !mbar_wait(b, (steps - 1) & 1, kDrainBudget);
-  dead = __syncthreads_or(dead);
-  tc_fence_after();
-  if (!dead) {
-    // row i of d_k in lane i (M = 128), or in lane 32 (i / 16) + i % 16 (M = 64)
-    const int quarter = warp % 4;
-    const int row = k0 + (M == 128 ? quarter * 32 + lane : quarter * 16 + lane);
-    const uint32_t lanes = tm + (static_cast<uint32_t>(quarter * 32) << 16);
-    float* w = a.w + (static_cast<int64_t>(blockIdx.x) * a.kv + h) * a.d_k * a.d_v;
-#pragma unroll
-    for (int c = (warp / 4) * 32; c < NV; c += C::kThreads / 4) {
-      uint32_t r[2][16];
-      tmem_ld_wait(lanes + c, r);
-      if (M == 128 || lane < 16) {
-#pragma unroll
-        for (int e = 0; e < 32; e += 8) {
-          uint32_t x[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) x[j] = r[e / 16][e % 16 + j];
-          st_global_v8(w + blocked(row, v0 + c + e, a.d_k), x);
-        }
-      }
-    }
-  }
-  tc_fence_before();
-  __syncthreads();
-  if (warp == 0) {
-    tc_fence_after();
-    tmem_dealloc(tm, C::kCols);
-  }
-}
-
-// ---- state of whole sequences ----------------------------------------------------------------
-// CTA = (sequence, key/value head, up to 128 rows of d_k x NV columns of d_v): the chunks in order, the
-// fp32 state in registers (at most 64 values a thread); before each chunk its fp16 rounding goes to
-// r16, after the last the state goes to the pool.  No W, no scan.  Steps of 64 tokens run through a
-// ring of three: one warp fetches (TMA: k, v, and the step's rotations), the data warps rotate k and cut
-// it in place and, every second step, add and round the chunk before while the products run, one warp
-// issues the products.  A data warp that also issued them held the others up for as long as they ran.
-template <int M, int NV>
-struct SeqCfg {
-  static constexpr int kData = NV == 256 ? 512 : 256;
-  static constexpr int kThreads = kData + 128;    // a warpgroup for the copying and the issuing warp
-  static constexpr int kHold = NV * 128 / kData;  // state values a thread
+  static constexpr int kData = 512, kThreads = kData + 128;  // a warpgroup for the copying and the issuing warp
+  static constexpr int kHold = NV * 128 / kData;             // state values a thread
   static constexpr int kStep = 64;
   static constexpr int kPlane = kStep * M * 2, kVBytes = kStep * NV * 2, kTurns = kStep / 16 * M * 4;
   static constexpr int kSmem = 3 * kPlane + 4 * kPlane + 3 * kVBytes + 3 * kTurns + 1024;
   static constexpr int kCols = 2 * NV;
-  // 640 threads are launched with 96 registers each (61440); 512 x 112 + 128 x 24 = 60416 of them
-  static constexpr bool kMoveRegisters = kData == 512;
+  // 640 threads are launched with 96 registers each (61440); 512 x 112 + 128 x 32 are as many
 };
 
-template <int M, int NV>
-__global__ void __launch_bounds__(SeqCfg<M, NV>::kThreads, 1)
-    tc_sequence_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, TcPackedArgs a,
-                       HeadParams hp) {
-  using C = SeqCfg<M, NV>;
+template <int M, int NV, bool SEQ>
+__global__ void __launch_bounds__(StateCfg<M, NV>::kThreads, 1)
+    tc_state_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, TcPackedArgs a,
+                    HeadParams hp) {
+  using C = StateCfg<M, NV>;
   extern __shared__ unsigned char raw_smem[];
   // products of even / odd steps done; operands of even / odd steps ready; ring slots filled, free
   __shared__ uint64_t bars[10];
   __shared__ uint32_t tmem_at;
   pdl_wait();
   pdl_go();
-  const int seq = blockIdx.x, h = blockIdx.y, slices = a.d_v / NV;
-  const int64_t u0 = a.cu[seq] / kChunk + seq;
-  if (u0 < 0 || u0 >= a.units) return;  // cu_seqlens out of order: no run has tokens
-  const RunDesc d = a.desc[u0];
-  if (d.tokens == 0 || d.seq != seq) return;
-  const int len = (d.runs - 1) * kChunk + a.desc[u0 + d.runs - 1].tokens, steps = (len + C::kStep - 1) / C::kStep;
+  const int slices = a.d_v / NV;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int k0 = (blockIdx.z / slices) * M, v0 = (blockIdx.z % slices) * NV;
-  const uint32_t sm = (smem_addr(raw_smem) + 1023u) & ~1023u, s2 = sm + 3 * C::kPlane, sv = s2 + 4 * C::kPlane,
-                 st_turns = sv + 3 * C::kVBytes;
+  // The CTA's chunks: units first .. first + count - 1 of head blockIdx.y, or the items blockIdx.x +
+  // i gridDim.x of (head, unit).
+  int64_t first = 0, count = 0;
+  RunDesc d0{};
+  if constexpr (SEQ) {
+    first = a.cu[blockIdx.x] / kChunk + blockIdx.x;
+    if (first < 0 || first >= a.units) return;  // cu_seqlens out of order: no run has tokens
+    d0 = a.desc[first];
+    if (d0.tokens == 0 || d0.seq != static_cast<int>(blockIdx.x)) return;
+    count = d0.runs;
+  } else {
+    const int64_t items = a.units * a.kv;
+    count = (items - blockIdx.x + gridDim.x - 1) / gridDim.x;
+  }
+  // Chunk i: its unit and head, and its tokens (0: none).
+  struct Item {
+    int64_t unit;
+    int head, tokens, row;
+  };
+  auto item = [&](int64_t i) {
+    Item it;
+    if constexpr (SEQ) {
+      it.unit = first + i;
+      it.head = blockIdx.y;
+      it.row = d0.row + static_cast<int>(i) * kChunk;
+      it.tokens = i + 1 < count ? kChunk : a.desc[it.unit].tokens;
+    } else {
+      const int64_t n = blockIdx.x + i * gridDim.x;
+      it.unit = n % a.units;
+      it.head = static_cast<int>(n / a.units);
+      const RunDesc d = a.desc[it.unit];
+      it.tokens = d.tokens;
+      it.row = d.row;
+    }
+    return it;
+  };
+  unsigned char* smem = raw_smem + ((1024u - (smem_addr(raw_smem) & 1023u)) & 1023u);
+  const uint32_t sm = smem_addr(smem), s2 = sm + 3 * C::kPlane, sv = s2 + 4 * C::kPlane, s_turns = sv + 3 * C::kVBytes;
   const uint32_t b_done = smem_addr(&bars[0]), b_ready = smem_addr(&bars[2]), b_full = smem_addr(&bars[4]),
                  b_free = smem_addr(&bars[7]);
   if (warp == 0) {
     tmem_alloc(smem_addr(&tmem_at), C::kCols);
-    tmem_relinquish();
+    tmem_relinquish();  // or another CTA of the SM waits for this one's end
   }
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -360,154 +241,211 @@ __global__ void __launch_bounds__(SeqCfg<M, NV>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tm = tmem_at;
-  auto slot_of = [](int st) { return st % 3; };
-  auto products_done = [&](int st) { return mbar_wait(b_done + 8 * (st & 1), (st >> 1) & 1, kDrainBudget); };
-  auto filled = [&](int st) { return mbar_wait(b_full + 8 * slot_of(st), (st / 3) & 1, kDrainBudget); };
+  // n: steps of this CTA so far
+  auto products_done = [&](int n) { return mbar_wait(b_done + 8 * (n & 1), (n >> 1) & 1, kDrainBudget); };
+  auto filled = [&](int n) { return mbar_wait(b_full + 8 * (n % 3), (n / 3) & 1, kDrainBudget); };
 
   if (tid >= C::kData) {
-    if constexpr (C::kMoveRegisters) registers_less<24>();
+    registers_less<32>();
     if (warp == C::kData / 32) {  // ---- products
       if (lane == 0) {
         constexpr uint32_t ID = idesc_bf16_f32(M, NV, 1, 1);
-        int st = 0;
-        for (; st < steps; ++st) {
-          if (!mbar_wait(b_ready + 8 * (st & 1), (st >> 1) & 1, kDrainBudget)) break;
-          tc_fence_after();
-          const uint64_t dv = sdesc_sw128(sv + slot_of(st) * C::kVBytes, C::kStep * 128, 1024);
-          const uint64_t d0 = sdesc_sw128(sm + slot_of(st) * C::kPlane, C::kStep * 128, 1024);
-          const uint64_t d1 = sdesc_sw128(s2 + (st & 1) * 2 * C::kPlane, C::kStep * 128, 1024);
-          const uint32_t tD = tm + ((st >> 1) & 1) * NV;
+        int n = 0, chunk = 0;
+        bool alive = true;
+        for (int64_t i = 0; alive && i < count; ++i) {
+          const int tokens = item(i).tokens;
+          for (int st = 0; st * C::kStep < tokens; ++st, ++n) {
+            if (!(alive = mbar_wait(b_ready + 8 * (n & 1), (n >> 1) & 1, kDrainBudget))) break;
+            tc_fence_after();
+            const uint64_t dv = sdesc_sw128(sv + n % 3 * C::kVBytes, C::kStep * 128, 1024);
+            const uint64_t dk0 = sdesc_sw128(sm + n % 3 * C::kPlane, C::kStep * 128, 1024);
+            const uint64_t dk1 = sdesc_sw128(s2 + (n & 1) * 2 * C::kPlane, C::kStep * 128, 1024);
+            const uint32_t tD = tm + (chunk & 1) * NV;
 #pragma unroll
-          for (int p = 2; p >= 0; --p) {  // the small planes first
-            const uint64_t dk = p == 0 ? d0 : d1 + (((p - 1) * C::kPlane) >> 4);
+            for (int p = 2; p >= 0; --p) {  // the small planes first
+              const uint64_t dk = p == 0 ? dk0 : dk1 + (((p - 1) * C::kPlane) >> 4);
 #pragma unroll
-            for (int ks = 0; ks < C::kStep / 16; ++ks)
-              mma_f16_ss(tD, dk + ((ks * 2048) >> 4), dv + ((ks * 2048) >> 4), ID, st % 2 || p < 2 || ks > 0);
+              for (int ks = 0; ks < C::kStep / 16; ++ks)
+                mma_f16_ss(tD, dk + ((ks * 2048) >> 4), dv + ((ks * 2048) >> 4), ID, st > 0 || p < 2 || ks > 0);
+            }
+            mma_commit(b_done + 8 * (n & 1));
+            mma_commit(b_free + 8 * (n % 3));
           }
-          mma_commit(b_done + 8 * (st & 1));
-          mma_commit(b_free + 8 * slot_of(st));
+          chunk += tokens > 0;
         }
-        for (int i = st > 3 ? st - 3 : 0; i < st; ++i) mbar_wait(b_free + 8 * slot_of(i), (i / 3) & 1, kDrainBudget);
+        for (int i = n > 3 ? n - 3 : 0; i < n; ++i) mbar_wait(b_free + 8 * (i % 3), (i / 3) & 1, kDrainBudget);
       }
     } else if (warp == C::kData / 32 + 1) {  // ---- copies
       if (lane == 0) {
-        int st = 0;
-        for (; st < steps; ++st) {
-          const int slot = slot_of(st);
-          if (st >= 3 && !mbar_wait(b_free + 8 * slot, (st / 3 - 1) & 1, kDrainBudget)) break;
-          const uint32_t bar = b_full + 8 * slot;
-          mbar_arrive_expect_tx(bar, C::kPlane + C::kVBytes + C::kTurns);
-          const int row = d.row + st * C::kStep;
-#pragma unroll
-          for (int c = 0; c < M; c += 64)
-            tma_load_2d(sm + slot * C::kPlane + c * (C::kStep * 2), &map_k, bar, h * a.d_k + k0 + c, row);
-#pragma unroll
-          for (int c = 0; c < NV; c += 64)
-            tma_load_2d(sv + slot * C::kVBytes + c * (C::kStep * 2), &map_v, bar, h * a.d_v + v0 + c, row);
-#pragma unroll
-          for (int i = 0; i < C::kStep / 16; ++i)
-            bulk_load(st_turns + slot * C::kTurns + i * M * 4,
-                      a.base + (u0 * 8 + st * (C::kStep / 16) + i) * static_cast<int64_t>(a.d_k) + k0, M * 4, bar);
+        prefetch_tensormap(&map_k);
+        prefetch_tensormap(&map_v);
+        int n = 0;
+        bool alive = true;
+        for (int64_t i = 0; alive && i < count; ++i) {
+          const Item it = item(i);
+          for (int st = 0; st * C::kStep < it.tokens; ++st, ++n) {
+            const int slot = n % 3;
+            if (n >= 3 && !(alive = mbar_wait(b_free + 8 * slot, (n / 3 - 1) & 1, kDrainBudget))) break;
+            const uint32_t bar = b_full + 8 * slot;
+            mbar_arrive_expect_tx(bar, C::kPlane + C::kVBytes + C::kTurns);
+            const int row = it.row + st * C::kStep;
+            tma_load_3d(sm + slot * C::kPlane, &map_k, bar, 0, row, (it.head * a.d_k + k0) / 64);
+            tma_load_3d(sv + slot * C::kVBytes, &map_v, bar, 0, row, (it.head * a.d_v + v0) / 64);
+            bulk_load(s_turns + slot * C::kTurns, a.base + (it.unit * a.d_k + k0) * 8 + st * (C::kStep / 16) * M, C::kTurns, bar);
+          }
         }
-        for (int i = st > 3 ? st - 3 : 0; i < st; ++i) filled(i);  // no copy in flight at the end
+        for (int i = n > 3 ? n - 3 : 0; i < n; ++i) filled(i);  // no copy in flight at the end
       }
     }
   } else {  // ---- data
-    if constexpr (C::kMoveRegisters) registers_more<112>();
+    registers_more<112>();
     constexpr int kGroups = M / 8, kRows = C::kData / kGroups, kPer = C::kStep / kRows;
     static_assert(kRows % 16 == 0, "a thread's rows share their place in a group of 16 tokens");
     const int g = tid % kGroups, tr = tid / kGroups;
     const uint32_t mine = (g / 8) * (C::kStep * 128) + sw128(tr, g % 8);  // kRows more rows: kRows * 128 bytes on
-    const float lg = hp.log2g[h];
-    const Turn off = scaled(load_turn(a.offset + (tr % 16) * a.d_k + k0 + g * 8), decay_pow(lg, 15 - tr % 16));
-    // this thread's piece of the state: row (k0 + row), columns v0 + cols on
+    const Turn off = load_turn(a.offset + (tr % 16) * a.d_k + k0 + g * 8);
+    // this thread's piece of the state: row i of d_k in lane i (M = 128), or in lane 32 (i / 16) + i % 16
+    // (M = 64); columns cols on
     const int quarter = warp % 4, cols = v0 + (warp / 4) * C::kHold;
     const bool holds = M == 128 || lane < 16;
     const int row = k0 + (M == 128 ? quarter * 32 + lane : quarter * 16 + lane % 16);
-    const int64_t state_size = static_cast<int64_t>(a.kv) * a.d_k * a.d_v, at_head = static_cast<int64_t>(h) * a.d_k * a.d_v;
-    float* pool = a.pool + d.slot * state_size + at_head + static_cast<int64_t>(row) * a.d_v + cols;
-    __half* r16 = a.r16 + u0 * state_size + at_head + blocked(row, cols, a.d_k);
-    float S[C::kHold];
-#pragma unroll
-    for (int e = 0; e < C::kHold; e += 4) {
-      const float4 x = d.pos > 0 && holds ? *reinterpret_cast<const float4*>(pool + e) : make_float4(0.f, 0.f, 0.f, 0.f);
-      S[e] = x.x; S[e + 1] = x.y; S[e + 2] = x.z; S[e + 3] = x.w;
-    }
-    __half2 mx = __float2half2_rn(0.f);
-    auto emit = [&](int chunk) {
+    const uint32_t t_mine = tm + (static_cast<uint32_t>(quarter * 32) << 16) + (warp / 4) * C::kHold;
+    const int64_t head_size = static_cast<int64_t>(a.d_k) * a.d_v, state_size = a.kv * head_size;
+    const int64_t at = blocked(row, cols, a.d_k);
+    float mx = 0.f;
+    Two S[SEQ ? C::kHold / 2 : 1];
+    float lg = 0.f, full_less = 0.f;
+    float* pool = nullptr;
+    __half* r16 = nullptr;
+    auto emit = [&](int64_t chunk) {  // the state before chunk `chunk`, rounded
       __half* to = r16 + chunk * state_size;
 #pragma unroll
       for (int e = 0; e < C::kHold; e += 8) {
         uint32_t w[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          w[j] = pack_f16x2(S[e + 2 * j], S[e + 2 * j + 1]);
-          track(mx, w[j]);
+          const float2 x = parts(S[e / 2 + j]);
+          track(mx, x.x, x.y);
+          w[j] = pack_f16x2(x.x, x.y);
         }
         if (holds) *reinterpret_cast<uint4*>(to + static_cast<int64_t>(e) * a.d_k) = make_uint4(w[0], w[1], w[2], w[3]);
       }
     };
-    if (d.pos > 0) emit(0);
-    // S <- S + less S + up D, D the products of a chunk
-    auto add_chunk = [&](int chunk, float less, float up) {
+    // S <- S + less S + up D, D the products of the CTA's chunk-th chunk; or D to W of (unit, head)
+    auto take = [&](int chunk, float less, float up, int64_t unit, int head) {
       tc_fence_after();
+      float* w = nullptr;
+      if constexpr (!SEQ) w = a.w + (unit * a.kv + head) * head_size + at;
 #pragma unroll
       for (int e = 0; e < C::kHold; e += 16) {
         uint32_t r[1][16];
-        tmem_ld_wait(tm + (static_cast<uint32_t>(quarter * 32) << 16) + (chunk & 1) * NV + (warp / 4) * C::kHold + e, r);
+        tmem_ld_wait(t_mine + (chunk & 1) * NV + e, r);
+        if constexpr (SEQ) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j) S[e + j] = fmaf(less, S[e + j], fmaf(up, __uint_as_float(r[0][j]), S[e + j]));
+          for (int j = 0; j < 8; ++j) {
+            Two& x = S[e / 2 + j];
+            x = fma2(two(less), x, fma2(two(up), two(__uint_as_float(r[0][2 * j]), __uint_as_float(r[0][2 * j + 1])), x));
+          }
+        } else if (holds) {
+#pragma unroll
+          for (int j = 0; j < 16; j += 8) {
+            uint32_t x[8];
+#pragma unroll
+            for (int m = 0; m < 8; ++m) x[m] = r[0][j + m];
+            st_global_v8(w + static_cast<int64_t>(e + j) * a.d_k, x);
+          }
+        }
       }
       tc_fence_before();
     };
-    const float full_less = decay_less_one(lg, kChunk);
+    float decays[2 * kPer];  // gamma^(127-t) of this thread's rows
+    auto set_head = [&](int head) {
+      lg = hp.log2g[head];
+#pragma unroll
+      for (int r = 0; r < 2 * kPer; ++r) decays[r] = decay_pow(lg, 127 - tr - r * kRows);
+    };
+    if constexpr (SEQ) {
+      set_head(blockIdx.y);
+      full_less = decay_less_one(lg, kChunk);
+      pool = a.pool + d0.slot * state_size + blockIdx.y * head_size + static_cast<int64_t>(row) * a.d_v + cols;
+      r16 = a.r16 + first * state_size + blockIdx.y * head_size + at;
+#pragma unroll
+      for (int e = 0; e < C::kHold; e += 4) {
+        const float4 x = d0.pos > 0 && holds ? *reinterpret_cast<const float4*>(pool + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+        S[e / 2] = two(x.x, x.y);
+        S[e / 2 + 1] = two(x.z, x.w);
+      }
+      if (d0.pos > 0) emit(0);
+    }
+    int n = 0, chunk = 0, last_step = -1;  // steps, chunks so far; the last step of the chunk before
+    int64_t last_unit = 0;
+    int last_head = 0, last_tokens = 0;
     bool alive = true;
-    for (int st = 0; st < steps; ++st) {
-      // the step's copies have landed; the small planes of two steps ago have been read
-      if (!(alive = (st < 2 || products_done(st - 2)) && filled(st))) break;
-      const int slot = slot_of(st), left = len - st * C::kStep;
-      const uint32_t hi = sm + slot * C::kPlane + mine, low = s2 + (st & 1) * 2 * C::kPlane + mine;
+    for (int64_t i = 0; alive && i < count; ++i) {
+      const Item it = item(i);
+      if (it.tokens == 0) continue;
+      if constexpr (!SEQ) set_head(it.head);
+      for (int st = 0; st * C::kStep < it.tokens; ++st, ++n) {
+        // the step's copies have landed; the small planes of two steps ago have been read
+        if (!(alive = (n < 2 || products_done(n - 2)) && filled(n))) break;
+        const int slot = n % 3, left = it.tokens - st * C::kStep;
+        unsigned char* hi = smem + slot * C::kPlane + mine;
+        unsigned char* low = smem + (3 + (n & 1) * 2) * C::kPlane + mine;
+        const unsigned char* turns = smem + 7 * C::kPlane + 3 * C::kVBytes + slot * C::kTurns + g * 32;
+        uint4 raw[kPer];
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int t = tr + i * kRows;
-        const uint32_t o = i * kRows * 128;
-        const uint32_t at = st_turns + slot * C::kTurns + (t / 16) * (M * 4) + g * 32;
-        const uint4 c = ld_shared_u4(at), s = ld_shared_u4(at + 16);
-        const Turn base{{static_cast<Two>(c.y) << 32 | c.x, static_cast<Two>(c.w) << 32 | c.z},
-                        {static_cast<Two>(s.y) << 32 | s.x, static_cast<Two>(s.w) << 32 | s.z}};
-        uint4 raw = ld_shared_u4(hi + o);
-        if (t >= left) raw = make_uint4(0, 0, 0, 0);  // rows behind the sequence
-        Eight y = turned(raw, product(scaled(base, decay_pow(lg, 112 - 64 * (st & 1) - t / 16 * 16)), off));
-        store_plane(hi + o, y);
-        store_plane(low + o, y);
-        store_plane(low + C::kPlane + o, y);
-      }
-      if (left < C::kStep) {  // 0 x v of another sequence may not be 0
-        for (int e = tid; e < (C::kStep - left) * (NV / 8); e += C::kData)
-          st_shared_v4(sv + slot * C::kVBytes + (e % (NV / 8) / 8) * (C::kStep * 128) + (left + e / (NV / 8)) * 128 + e % 8 * 16, 0, 0, 0, 0);
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(b_ready + 8 * (st & 1));
-      if (st >= 3 && st % 2) {  // (awaited above) the products of chunk st / 2 - 1
-        add_chunk(st / 2 - 1, full_less, 1.f);
-        emit(st / 2);
-      }
-    }
-    if (alive && steps % 2 && steps > 1 && (alive = products_done(steps - 2))) {
-      add_chunk(d.runs - 2, full_less, 1.f);
-      emit(d.runs - 1);
-    }
-    if (alive && products_done(steps - 1)) {
-      const int last = len - (d.runs - 1) * kChunk;
-      add_chunk(d.runs - 1, decay_less_one(lg, last), exp2f(static_cast<float>(last - kChunk) * lg));
-      if (holds) {
+        for (int r = 0; r < kPer; ++r) {
+          raw[r] = *reinterpret_cast<const uint4*>(hi + r * kRows * 128);
+        }
+        if (left < C::kStep) {  // rows behind the sequence
 #pragma unroll
-        for (int e = 0; e < C::kHold; e += 4)
-          *reinterpret_cast<float4*>(pool + e) = make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);
+          for (int r = 0; r < kPer; ++r)
+            if (tr + r * kRows >= left) raw[r] = make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int r = 0; r < kPer; ++r) {
+          const int t = tr + r * kRows, o = r * kRows * 128;
+          const Turn base = load_turn(reinterpret_cast<const float*>(turns + t / 16 * (M * 4)));
+          Eight y = turned(raw[r], product(scaled(base, st ? decays[kPer + r] : decays[r]), off));
+          store_plane(hi + o, y);
+          store_plane(low + o, y);
+          store_plane(low + C::kPlane + o, y);
+        }
+        if (left < C::kStep) {  // 0 x v of another sequence may not be 0
+          for (int e = tid; e < (C::kStep - left) * (NV / 8); e += C::kData)
+            st_shared_v4(sv + slot * C::kVBytes + (e % (NV / 8) / 8) * (C::kStep * 128) + (left + e / (NV / 8)) * 128 + e % 8 * 16,
+                         0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b_ready + 8 * (n & 1));
+      }
+      if (!alive) break;
+      if (chunk > 0) {  // its products ran beside this chunk's first steps
+        if (!(alive = products_done(last_step))) break;
+        take(chunk - 1, full_less, 1.f, last_unit, last_head);
+        if constexpr (SEQ) emit(i);
+      }
+      ++chunk;
+      last_step = n - 1;
+      last_unit = it.unit;
+      last_head = it.head;
+      last_tokens = it.tokens;
+    }
+    if (alive && chunk > 0 && products_done(last_step)) {
+      take(chunk - 1, SEQ ? decay_less_one(lg, last_tokens) : 0.f,
+           SEQ ? exp2f(static_cast<float>(last_tokens - kChunk) * lg) : 1.f, last_unit, last_head);
+      if constexpr (SEQ) {
+        if (holds) {
+#pragma unroll
+          for (int e = 0; e < C::kHold; e += 4) {
+            const float2 x = parts(S[e / 2]), y = parts(S[e / 2 + 1]);
+            *reinterpret_cast<float4*>(pool + e) = make_float4(x.x, x.y, y.x, y.y);
+          }
+        }
       }
     }
-    report(mx);
+    if constexpr (SEQ) report_fp16_range(mx);
   }
   tc_fence_before();
   __syncthreads();
@@ -540,7 +478,7 @@ __global__ void __launch_bounds__(kScanThreads) tc_scan_kernel(TcPackedArgs a, H
   const int64_t step = static_cast<int64_t>(a.kv) * n4;
   const float4* w = reinterpret_cast<const float4*>(a.w) + (u0 * a.kv + h) * n4 + e;
   uint2* r16 = reinterpret_cast<uint2*>(a.r16) + (u0 * a.kv + h) * n4 + e;
-  __half2 mx = __float2half2_rn(0.f);
+  float mx = 0.f;
   constexpr int kAhead = 4;
   for (int i0 = 0; i0 < first.runs; i0 += kAhead) {
     float4 x[kAhead];
@@ -552,10 +490,9 @@ __global__ void __launch_bounds__(kScanThreads) tc_scan_kernel(TcPackedArgs a, H
       const int u = i0 + i;
       if (u >= first.runs) break;
       if (u > 0 || first.pos > 0) {
-        const uint32_t lo = pack_f16x2(r.x, r.y), hi = pack_f16x2(r.z, r.w);
-        track(mx, lo);
-        track(mx, hi);
-        r16[u * step] = make_uint2(lo, hi);
+        track(mx, r.x, r.y);
+        track(mx, r.z, r.w);
+        r16[u * step] = make_uint2(pack_f16x2(r.x, r.y), pack_f16x2(r.z, r.w));
       }
       float less = full_less, up = 1.f;
       if (u + 1 == first.runs) {
@@ -570,7 +507,7 @@ __global__ void __launch_bounds__(kScanThreads) tc_scan_kernel(TcPackedArgs a, H
     }
   }
   *slot = r;
-  report(mx);
+  report_fp16_range(mx);
 }
 
 // ---- output ----------------------------------------------------------------------------------
@@ -617,7 +554,8 @@ __global__ void __launch_bounds__(OutCfg<DK>::kThreads, OutCfg<DK>::kCtas) tc_ou
   }
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int hq = blockIdx.y, h = hq / a.group, slices = a.d_v / NV;
-  const uint32_t sq = (smem_addr(raw_smem) + 1023u) & ~1023u, sk = sq + C::kQ, own = sk + C::kQ;
+  unsigned char* smem = raw_smem + ((1024u - (smem_addr(raw_smem) & 1023u)) & 1023u);
+  const uint32_t sq = smem_addr(smem), sk = sq + C::kQ, own = sk + C::kQ;
   const uint32_t b_qk = smem_addr(bars), b_s = b_qk + 8, b_p = b_qk + 16, b_full = b_qk + 24, b_done = b_full + 8 * C::kRing,
                  b_read = b_done + 8 * C::kTeams;
   const bool has_r = !(d.index == 0 && d.pos == 0);
@@ -749,38 +687,42 @@ __global__ void __launch_bounds__(OutCfg<DK>::kThreads, OutCfg<DK>::kCtas) tc_ou
     for (int i = s > C::kRing ? s - C::kRing : 0; i < s; ++i) wait(b_full + 8 * (i % C::kRing), i / C::kRing);
   } else {  // ---- data
     const float lg = hp.log2g[h];
+    constexpr int kBase = DK < 128 ? DK : 128;  // columns of a block of the rotations
     // rows t = tr + kRows i: each one's rotation is the last one's times a constant step
-    const Turn first = product(load_turn_l2(a.base + (static_cast<int64_t>(blockIdx.x) * 8 + tr / 16) * DK + g * 8),
+    const Turn first = product(load_turn_l2(a.base + (static_cast<int64_t>(blockIdx.x) * DK + g * 8 / kBase * kBase) * 8 +
+                                            tr / 16 * kBase + g * 8 % kBase),
                                load_turn_l2(a.offset + (tr % 16) * DK + g * 8));
     Turn step = load_turn_l2(a.offset + 16 * DK + g * 8);
     if (kRows == 32) step = product(step, step);
-    __half2 mx = __float2half2_rn(0.f);
+    float mx = 0.f;
     // q by gamma^(t+1), k by gamma^(127-t)
-    auto convert = [&](uint32_t area, float scale, float grow) {
+    auto convert = [&](unsigned char* area, float scale, float grow) {
       Turn t = scaled(first, scale);
       const Turn by = scaled(step, grow);
+      uint4 raw[kPer];
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) raw[i] = *reinterpret_cast<const uint4*>(area + mine + i * kRows * 128);
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        const uint32_t to = area + mine + i * kRows * 128;
-        const Eight y = turned(ld_shared_u4(to), t);
+        const Eight y = turned(raw[i], t);
         uint32_t w[4];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const float2 u = parts(y.first[e]), v = parts(y.second[e]);
+          track(mx, u.x, u.y);
+          track(mx, v.x, v.y);
           w[2 * e] = pack_f16x2(u.x, v.x);
           w[2 * e + 1] = pack_f16x2(u.y, v.y);
-          track(mx, w[2 * e]);
-          track(mx, w[2 * e + 1]);
         }
-        st_shared_v4(to, w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(area + mine + i * kRows * 128) = make_uint4(w[0], w[1], w[2], w[3]);
         if (i + 1 < kPer) t = product(t, by);
       }
     };
     cp_async_wait<1>();
-    convert(sq, decay_pow(lg, tr + 1), decay_pow(lg, kRows));
+    convert(smem, decay_pow(lg, tr + 1), decay_pow(lg, kRows));
     cp_async_wait<0>();
-    convert(sk, decay_pow(lg, kChunk - 1 - tr), exp2f(-static_cast<float>(kRows) * lg));
-    report(mx);
+    convert(smem + C::kQ, decay_pow(lg, kChunk - 1 - tr), exp2f(-static_cast<float>(kRows) * lg));
+    report_fp16_range(mx);
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(b_qk);
@@ -859,29 +801,23 @@ cudaError_t prepare(K kernel, int smem) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
 }
 
-template <int M, int NV>
-cudaError_t launch_sequences(const PackedCall& c, const TcPackedArgs& a, const HeadParams& hp, cudaStream_t s) {
-  using C = SeqCfg<M, NV>;
-  const cudaError_t e = prepare(tc_sequence_kernel<M, NV>, C::kSmem);
+template <int M, int NV, bool SEQ>
+cudaError_t launch_states(const PackedCall& c, const TcPackedArgs& a, const HeadParams& hp, cudaStream_t s) {
+  using C = StateCfg<M, NV>;
+  cudaError_t e = prepare(tc_state_kernel<M, NV, SEQ>, C::kSmem);
   if (e != cudaSuccess) return e;
   CUtensorMap mk, mv;
-  if (!encode_token_rows(&mk, c.k, c.rows, c.heads_kv * c.d_k, c.stride_k, C::kStep) ||
-      !encode_token_rows(&mv, c.v, c.rows, c.heads_kv * c.d_v, c.stride_v, C::kStep))
+  if (!encode_token_rows(&mk, c.k, c.rows, c.heads_kv * c.d_k, c.stride_k, C::kStep, M / 64) ||
+      !encode_token_rows(&mv, c.v, c.rows, c.heads_kv * c.d_v, c.stride_v, C::kStep, NV / 64))
     return cudaErrorUnknown;
-  return launch_dependent(tc_sequence_kernel<M, NV>,
-                          dim3(static_cast<unsigned>(c.seqs), static_cast<unsigned>(a.kv),
-                               static_cast<unsigned>((a.d_k / M) * (a.d_v / NV))),
-                          dim3(C::kThreads), C::kSmem, s, mk, mv, a, hp);
-}
-template <int M, int NV>
-cudaError_t launch_chunks(const PackedCall& c, const TcPackedArgs& a, const HeadParams& hp, cudaStream_t s) {
-  using C = StateCfg<M, NV>;
-  cudaError_t e = prepare(tc_state_kernel<M, NV>, C::kSmem);
-  if (e != cudaSuccess) return e;
-  const unsigned kv = static_cast<unsigned>(a.kv);
-  e = launch_dependent(tc_state_kernel<M, NV>,
-                       dim3(static_cast<unsigned>(a.units), kv, static_cast<unsigned>((a.d_k / M) * (a.d_v / NV))),
-                       dim3(C::kThreads), C::kSmem, s, a, hp);
+  const unsigned kv = static_cast<unsigned>(a.kv), z = static_cast<unsigned>((a.d_k / M) * (a.d_v / NV));
+  const dim3 block(C::kThreads);
+  if (SEQ)
+    return launch_dependent(tc_state_kernel<M, NV, SEQ>, dim3(static_cast<unsigned>(c.seqs), kv, z), block, C::kSmem, s, mk,
+                            mv, a, hp);
+  const int64_t items = a.units * a.kv, most = std::max<int64_t>(1, 148 / z);
+  e = launch_dependent(tc_state_kernel<M, NV, SEQ>, dim3(static_cast<unsigned>(std::min(items, most)), 1, z), block, C::kSmem, s,
+                       mk, mv, a, hp);
   if (e != cudaSuccess) return e;
   const unsigned nb = static_cast<unsigned>((static_cast<int64_t>(a.d_k) * a.d_v / 4 + kScanThreads - 1) / kScanThreads);
   return launch_dependent(tc_scan_kernel, dim3(nb, kv, static_cast<unsigned>(c.seqs)), dim3(kScanThreads), 0, s, a, hp);
@@ -891,10 +827,10 @@ cudaError_t launch_chunks(const PackedCall& c, const TcPackedArgs& a, const Head
 // more pass over every chunk's fp32 state, written and read (at d_k 256, d_v 512 more bytes than q, k,
 // v and o together); a sequence's walk takes the time of its longest one, so it needs enough CTAs to
 // fill the GPU, or sequences short enough (two chunks on average) that there is nothing to spread.
-int sequence_columns(int64_t d_v) { return d_v % 256 == 0 ? 256 : d_v % 128 == 0 ? 128 : 64; }
+int state_columns(int64_t d_v) { return d_v % 256 == 0 ? 256 : d_v % 128 == 0 ? 128 : 64; }
 bool by_sequence(int64_t rows, int64_t seqs, int64_t heads_kv, int64_t d_k, int64_t d_v) {
   return rows <= 2 * kChunk * seqs ||
-         seqs * heads_kv * (d_k > 128 ? d_k / 128 : 1) * (d_v / sequence_columns(d_v)) >= 96;
+         seqs * heads_kv * (d_k > 128 ? d_k / 128 : 1) * (d_v / state_columns(d_v)) >= 96;
 }
 
 template <int DK>
@@ -903,12 +839,13 @@ cudaError_t launch_shape(const PackedCall& c, const TcPackedArgs& a, const HeadP
   using O = OutCfg<DK>;
   cudaError_t e = prepare(tc_output_kernel<DK>, O::kSmem);
   if (e != cudaSuccess) return e;
+  const int nv = state_columns(c.d_v);
   if (by_sequence(c.rows, c.seqs, c.heads_kv, c.d_k, c.d_v)) {
-    const int nv = sequence_columns(c.d_v);
-    e = nv == 256 ? launch_sequences<M, 256>(c, a, hp, s)
-                  : nv == 128 ? launch_sequences<M, 128>(c, a, hp, s) : launch_sequences<M, 64>(c, a, hp, s);
+    e = nv == 256 ? launch_states<M, 256, true>(c, a, hp, s)
+                  : nv == 128 ? launch_states<M, 128, true>(c, a, hp, s) : launch_states<M, 64, true>(c, a, hp, s);
   } else {
-    e = c.d_v % 128 == 0 ? launch_chunks<M, 128>(c, a, hp, s) : launch_chunks<M, 64>(c, a, hp, s);
+    e = nv == 256 ? launch_states<M, 256, false>(c, a, hp, s)
+                  : nv == 128 ? launch_states<M, 128, false>(c, a, hp, s) : launch_states<M, 64, false>(c, a, hp, s);
   }
   if (e != cudaSuccess) return e;
   return launch_dependent(tc_output_kernel<DK>, dim3(static_cast<unsigned>(a.units), static_cast<unsigned>(c.heads)),
