@@ -2,7 +2,8 @@
 
 The compute lives in the CUDA kernels behind the C interface ``include/retnet.h``; this
 module only marshals arguments (device pointers, sizes, dtype codes, the caller's stream)
-and turns a non-zero status into an exception.  PyTorch is used for device memory and
+and turns a non-zero status into an exception; the calls of a serving loop do that in a
+compiled module, _torch_binding, built beside the library.  PyTorch is used for device memory and
 streams.  There is no CPU path: if the library is missing, ``load()`` raises.
 
 The functions carry the C names:
@@ -19,9 +20,7 @@ The functions carry the C names:
 with the §三.3 normalisations chosen by flags.  Tensors are dense BLHD (see the header).
 """
 import ctypes
-import functools
 import os
-import struct
 
 import numpy as np
 
@@ -67,12 +66,6 @@ class Dims(ctypes.Structure):
 class PackedDims(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int64) for n in ("tokens", "seqs", "heads", "heads_kv", "d_k", "d_v", "slots", "stride_q",
                                               "stride_k", "stride_v", "stride_o")]
-    _pack = struct.Struct("11q").pack
-
-    @classmethod
-    def of(cls, *values):
-        """From all eleven values (a single copy: a third of the time of the field-wise constructor)."""
-        return cls.from_buffer_copy(cls._pack(*values))
 
 
 _lib = None
@@ -474,90 +467,33 @@ def retnet_fp16_range_errors(clear=True):
 
 # ---- serving: packed sequences over a pool of states ----------------------------------------
 
-def _values(a, n):
-    """Host float32 values as bytes, which ctypes passes as their address (the C calls read them before
-    they return; ndarray.ctypes.data_as costs microseconds a call)."""
-    arr = _host_f32(a, n)
-    return None if arr is None else arr.tobytes()
+_binding = None
 
 
-def _one_device(*ts):
-    """All tensors on one CUDA device: its index."""
-    dev = ts[0].get_device()
-    for t in ts:
-        if t is not None and t.get_device() != dev:
-            raise ValueError("tensors must be CUDA tensors of one device")
-    if dev < 0:
-        raise ValueError("tensors must be CUDA tensors of one device")
-    return dev
+def _native():
+    """The compiled tensor side (csrc/torch_binding.cpp), built beside the library."""
+    global _binding
+    if _binding is None:
+        import torch  # noqa: F401  (its libraries, before the module that needs them)
+        load()
+        from . import _torch_binding
+        _binding = _torch_binding
+    return _binding
 
 
-def _on(device, fn, stream):
-    """fn(raw stream) with ``device`` current (the C calls work on the current device); the stream
-    defaults to that device's current one."""
-    import torch
-    raw = torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
-    if torch.cuda.current_device() == device:
-        status = fn(raw)
-    else:
-        with torch.cuda.device(device):
-            status = fn(raw)
-    if status:
-        _check(status)
+def _host(a):
+    """A host parameter array as the compiled binding takes it (it converts other numpy types itself)."""
+    return a if a is None or type(a) is np.ndarray else _host_f32(a, 0)
 
 
-def _allocate(stream, fn):
-    """fn() -- torch.empty calls -- with ``stream`` current, so that the memory is that stream's: free for
-    it to write, and used again behind its work only."""
-    if stream is None:
-        return fn()
-    import torch
-    with torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream):
-        return fn()
-
-
-def _token_stride(t, name):
-    """Elements between the rows of (rows, heads, width), whose heads are contiguous."""
-    rows, heads, width = t.shape
-    sr, sh, sw = t.stride()
-    if (width > 1 and sw != 1) or (heads > 1 and sh != width) or (rows > 1 and sr < heads * width):
-        raise ValueError(f"{name}: the heads of a row must be contiguous, and rows must not overlap")
-    return sr if rows > 1 else heads * width
-
-
-def _index(t, dtype, n, name):
-    if t.dtype != dtype or t.shape != (n,) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} entries")
-    return t.data_ptr()
-
-
-def _packed_dims(q, k, v, o, pool, seqs):
-    import torch
-    # one look at each attribute: this is most of a small call's time
-    (rows, heads, dk), (v_rows, kv, dv), pool_shape, dtype = q.shape, v.shape, pool.shape, q.dtype
-    if k.shape != (rows, kv, dk) or v_rows != rows or o.shape != (rows, heads, dv):
-        raise ValueError("shape mismatch between q, k, v, o")
-    if k.dtype != dtype or v.dtype != dtype or o.dtype != dtype:
-        raise ValueError("q, k, v and o must have one dtype")
-    slots = pool_shape[0] if len(pool_shape) == 4 else 0
-    if pool.dtype != torch.float32 or pool_shape != (slots, kv, dk, dv) or not pool.is_contiguous():
-        raise ValueError("pool must be a contiguous float32 (slots, heads_kv, d_k, d_v)")
-    strides = []
-    for t, n, w, name in ((q, heads, dk, "q"), (k, kv, dk, "k"), (v, kv, dv, "v"), (o, heads, dv, "o")):
-        row, head, one = t.stride()
-        strides.append(row if one == 1 and head == w and row >= n * w else _token_stride(t, name))
-    return PackedDims.of(rows, seqs, heads, kv, dk, dv, slots, *strides)
+def _raw(stream):
+    return None if stream is None else _stream(stream)
 
 
 def retnet_packed_workspace_size(dims) -> int:
     """Bytes of workspace for retnet_retention_packed; dims = (tokens, seqs, heads, heads_kv, d_k, d_v)."""
-    return _packed_workspace_size(*dims)
-
-
-@functools.lru_cache(maxsize=1024)
-def _packed_workspace_size(rows, seqs, heads, kv, dk, dv):
     out = ctypes.c_size_t(0)
-    _check(load().retnet_packed_workspace_size(PackedDims(rows, seqs, heads, kv, dk, dv, 1), ctypes.byref(out)))
+    _check(load().retnet_packed_workspace_size(PackedDims(*(int(x) for x in dims), 1), ctypes.byref(out)))
     return out.value
 
 
@@ -570,22 +506,8 @@ def retnet_retention_packed(q, k, v, o, pool, cu_seqlens, slots, pos, gamma, the
     (seqs + 1,) int32, slots (seqs,) int32, pos (seqs,) int64 or None on the device; gamma (heads_kv,),
     theta (d_k/2,) on the host.  Sequence i starts at position pos[i]: 0 from a zero state, else from
     pool[slots[i]].  Without a workspace (uint8 CUDA tensor) one is allocated for the call."""
-    import torch
-    dev = _one_device(q, k, v, o, pool, cu_seqlens, slots, pos, workspace)
-    seqs = slots.shape[0]
-    d = _packed_dims(q, k, v, o, pool, seqs)
-    cu = _index(cu_seqlens, torch.int32, seqs + 1, "cu_seqlens")
-    sl = _index(slots, torch.int32, seqs, "slots")
-    ps = None if pos is None else _index(pos, torch.int64, seqs, "pos")
-    g, th = _values(gamma, d.heads_kv), _values(theta, d.d_k // 2)
-    if workspace is None:
-        size = _packed_workspace_size(d.tokens, seqs, d.heads, d.heads_kv, d.d_k, d.d_v)
-        workspace = _allocate(stream, lambda: torch.empty(size, dtype=torch.uint8, device=dev))
-    elif not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    _on(dev, lambda s: load().retnet_retention_packed(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), d, _dtype_code(q), g, th, int(flags),
-        cu, sl, ps, pool.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(), s), stream)
+    _check(_native().retention_packed(q, k, v, o, pool, cu_seqlens, slots, pos, _host(gamma), _host(theta), flags, workspace,
+                                      _raw(stream)))
 
 
 def retnet_retention_step_slots(q, k, v, o, pool, slots, pos, gamma, theta=None,
@@ -593,29 +515,13 @@ def retnet_retention_step_slots(q, k, v, o, pool, slots, pos, gamma, theta=None,
     """One token for each of the rows' sequences, into ``o`` and ``pool`` (in place): q (rows, heads, d_k),
     k (rows, heads_kv, d_k), v (rows, heads_kv, d_v), o (rows, heads, d_v); slots (rows,) int32 (negative:
     padding) and pos (rows,) int64 or None on the device; the rest as retnet_retention_packed."""
-    import torch
-    dev = _one_device(q, k, v, o, pool, slots, pos)
-    d = _packed_dims(q, k, v, o, pool, q.shape[0])
-    sl = _index(slots, torch.int32, d.seqs, "slots")
-    ps = None if pos is None else _index(pos, torch.int64, d.seqs, "pos")
-    g, th = _values(gamma, d.heads_kv), _values(theta, d.d_k // 2)
-    _on(dev, lambda s: load().retnet_retention_step_slots(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), d, _dtype_code(q), g, th, int(flags),
-        sl, ps, pool.data_ptr(), s), stream)
+    _check(_native().retention_step_slots(q, k, v, o, pool, slots, pos, _host(gamma), _host(theta), flags, _raw(stream)))
 
 
 def retnet_state_slots_copy(pool, src, dst, stream=None):
     """pool[dst[i]] <- the old pool[src[i]] for all pairs at once (zeros where src[i] < 0; dst[i] < 0 is
     padding): pool (slots, ...) float32, src and dst (pairs,) int32 on the device, up to MAX_SLOT_PAIRS."""
-    import torch
-    dev = _one_device(pool, src, dst)
-    if pool.dtype != torch.float32 or not pool.is_contiguous():
-        raise ValueError("pool must be a contiguous float32 tensor")
-    n = src.shape[0]
-    sp, dp = _index(src, torch.int32, n, "src"), _index(dst, torch.int32, n, "dst")
-    slots = pool.shape[0]
-    _on(dev, lambda s: load().retnet_state_slots_copy(pool.data_ptr(), slots, pool.numel() // max(slots, 1), sp, dp, n,
-                                                      s), stream)
+    _check(_native().state_slots_copy(pool, src, dst, _raw(stream)))
 
 
 def retnet_slot_errors(clear=True):
@@ -628,42 +534,16 @@ def retnet_slot_errors(clear=True):
 
 # ---- the MSR epilogue with a learnable affine ------------------------------------------------
 
-def _msr_args(y, params, *same):
-    import torch
-    shape, dtype = y.shape, y.dtype
-    if len(shape) != 3 or not y.is_contiguous():
-        raise ValueError("y must be a contiguous (tokens, heads, d_v)")
-    for t in same:
-        if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
-            raise ValueError("y, g, out, dout, dy and dg must be contiguous and have one shape and dtype")
-    head = shape[1:]
-    for t in params:
-        if t is not None and (t.shape != head or t.dtype != torch.float32 or not t.is_contiguous()):
-            raise ValueError("weight, bias, dweight and dbias must be contiguous float32 (heads, d_v)")
-    return _one_device(y, *same, *params)
-
-
-def _optional_ptr(t):
-    return None if t is None else t.data_ptr()
-
-
 def retnet_msr_affine(y, g, weight, bias, out, eps=1e-5, stream=None):
     """swish(g) * (weight * GroupNorm_h(y) + bias) into ``out``: y, g, out (tokens, heads, d_v) of one dtype,
     weight and bias (heads, d_v) float32 or None."""
-    dev = _msr_args(y, (weight, bias), g, out)
-    _on(dev, lambda s: load().retnet_msr_affine(y.data_ptr(), g.data_ptr(), _optional_ptr(weight), _optional_ptr(bias),
-                                                out.data_ptr(), *y.shape, float(eps), _dtype_code(y), s), stream)
+    _check(_native().msr_affine(y, g, weight, bias, out, eps, _raw(stream)))
 
 
 def retnet_msr_affine_workspace_size(shape) -> int:
     """Bytes of workspace for retnet_msr_affine_backward; shape = (tokens, heads, d_v)."""
-    return _msr_affine_workspace_size(*shape)
-
-
-@functools.lru_cache(maxsize=1024)
-def _msr_affine_workspace_size(tokens, heads, d_v):
     out = ctypes.c_size_t(0)
-    _check(load().retnet_msr_affine_workspace_size(tokens, heads, d_v, ctypes.byref(out)))
+    _check(load().retnet_msr_affine_workspace_size(*(int(x) for x in shape), ctypes.byref(out)))
     return out.value
 
 
@@ -671,20 +551,7 @@ def retnet_msr_affine_backward(y, g, weight, bias, dout, dy, dg, dweight=None, d
                                stream=None):
     """Gradient of retnet_msr_affine into dy, dg (shape and dtype of y) and, where given, dweight and dbias
     (heads, d_v) float32.  Without a workspace (uint8 CUDA tensor) one is allocated for the call."""
-    import torch
-    dev = _msr_args(y, (weight, bias, dweight, dbias), g, dout, dy, dg)
-    if workspace is None and (dweight is not None or dbias is not None):
-        size = _msr_affine_workspace_size(*y.shape)
-        workspace = _allocate(stream, lambda: torch.empty(size, dtype=torch.uint8, device=dev))
-    elif workspace is not None:
-        _one_device(y, workspace)
-        if not workspace.is_contiguous():
-            raise ValueError("workspace must be contiguous")
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _on(dev, lambda s: load().retnet_msr_affine_backward(
-        y.data_ptr(), g.data_ptr(), _optional_ptr(weight), _optional_ptr(bias), dout.data_ptr(), dy.data_ptr(),
-        dg.data_ptr(), _optional_ptr(dweight), _optional_ptr(dbias), *y.shape, float(eps), _dtype_code(y),
-        _optional_ptr(workspace), ws_bytes, s), stream)
+    _check(_native().msr_affine_backward(y, g, weight, bias, dout, dy, dg, dweight, dbias, eps, workspace, _raw(stream)))
 
 
 # ---- allocating conveniences (torch.empty for the outputs, then the calls above) ----------
@@ -708,17 +575,13 @@ def retention_parallel(q, k, v, gamma, theta=None, flags=F_ALL, pos0=0, out_dtyp
 
 
 def msr_affine(y, g, weight=None, bias=None, eps=1e-5, stream=None):
-    import torch
-    out = _allocate(stream, lambda: torch.empty_like(y))
-    retnet_msr_affine(y, g, weight, bias, out, eps, stream)
+    status, out = _native().msr_affine_new(y, g, weight, bias, eps, _raw(stream))
+    _check(status)
     return out
 
 
 def msr_affine_backward(y, g, weight, bias, dout, eps=1e-5, workspace=None, stream=None):
     """(dy, dg, dweight, dbias) of msr_affine."""
-    import torch
-    dy, dg, sums = _allocate(stream, lambda: (
-        torch.empty_like(y), torch.empty_like(g), torch.empty((2, *y.shape[1:]), dtype=torch.float32, device=y.device)))
-    dw, db = sums.unbind(0)
-    retnet_msr_affine_backward(y, g, weight, bias, dout, dy, dg, dw, db, eps, workspace, stream)
-    return dy, dg, dw, db
+    status, *grads = _native().msr_affine_backward_new(y, g, weight, bias, dout, eps, workspace, _raw(stream))
+    _check(status)
+    return tuple(grads)

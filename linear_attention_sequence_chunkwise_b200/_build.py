@@ -1,4 +1,4 @@
-"""Build libretnet.so (the C-ABI library and its sm_100a kernels) in-tree with nvcc."""
+"""Build libretnet.so (the C-ABI library and its sm_100a kernels) and its torch binding in-tree."""
 import glob
 import os
 import subprocess
@@ -8,6 +8,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libretnet.so")
+BINDING = os.path.join(PKG, "_torch_binding.so")  # torch tensors in, calls into libretnet.so out
+BINDING_SRC = os.path.join(CSRC, "torch_binding.cpp")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 NVCC_FLAGS = ["-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo",
@@ -23,16 +25,43 @@ def _deps():
                                + glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
+def _newer(target, deps) -> bool:
+    return os.path.exists(target) and all(os.path.getmtime(p) <= os.path.getmtime(target) for p in deps)
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
-        return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(p) <= t for p in _deps())
+    return _newer(LIB, _deps())
+
+
+def binding_up_to_date() -> bool:
+    return _newer(BINDING, [BINDING_SRC, *glob.glob(os.path.join(INCLUDE, "*.h"))])
+
+
+def _binding_command(out):
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    includes = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+                os.path.join(cuda, "include"), sysconfig.get_paths()["include"], INCLUDE]
+    return ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-w",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-DTORCH_EXTENSION_NAME=_torch_binding",
+            *[f"-I{d}" for d in includes], BINDING_SRC, "-o", out, f"-L{os.path.join(root, 'lib')}", "-lc10", "-lc10_cuda",
+            "-ltorch_cpu", "-ltorch", "-ltorch_python", f"-L{PKG}", "-l:libretnet.so", "-Wl,-rpath,$ORIGIN"]
+
+
+def _build_binding():
+    tmp = f"{BINDING}.{os.getpid()}.tmp"
+    subprocess.run(_binding_command(tmp), check=True)
+    os.replace(tmp, BINDING)
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    """Compile every csrc/*.cu for sm_100a and link libretnet.so; return its path."""
+    """Compile every csrc/*.cu for sm_100a and link libretnet.so, then the torch binding; return the library's path."""
     if not force and up_to_date():
+        if not binding_up_to_date():
+            _build_binding()
         return LIB
     nvcc = os.environ.get("NVCC", "nvcc")
     os.makedirs(BUILD_DIR, exist_ok=True)
@@ -54,6 +83,8 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     link = [nvcc, "-shared", "-gencode", "arch=compute_100a,code=sm_100a", *objs, "-o", tmp, "-cudart", "static"]
     subprocess.run(link, check=True)
     os.replace(tmp, LIB)
+    if force or not binding_up_to_date():
+        _build_binding()
     return LIB
 
 

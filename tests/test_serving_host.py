@@ -112,32 +112,46 @@ def test_msr_affine_refusals(lib):
 
 
 def test_binding_refusals():
-    """Wrong shapes, types, layouts and host tensors raise before the library is called."""
+    """Wrong shapes, types, layouts and host tensors raise before the library is called; where everything
+    else is right, host tensors are what is refused."""
     q, k, v, o = torch.zeros(4, 4, 16), torch.zeros(4, 2, 16), torch.zeros(4, 2, 8), torch.zeros(4, 4, 8)
     pool, cu = torch.zeros(5, 2, 16, 8), torch.zeros(3, dtype=torch.int32)
     sl, pos = torch.zeros(2, dtype=torch.int32), torch.zeros(2, dtype=torch.int64)
-    with pytest.raises(ValueError, match="CUDA tensors"):
-        rn.retnet_retention_packed(q, k, v, o, pool, cu, sl, pos, G2, TH8)
-    d = rn._packed_dims(q, k, v, o, pool, 2)
-    assert (d.tokens, d.seqs, d.heads, d.heads_kv, d.d_k, d.d_v, d.slots, d.stride_q) == (4, 2, 4, 2, 16, 8, 5, 64)
+    good = dict(q=q, k=k, v=v, o=o, pool=pool, cu_seqlens=cu, slots=sl, pos=pos, gamma=G2, theta=TH8)
     wide = torch.zeros(4, 200)
-    assert rn._token_stride(wide[:, 3:67].unflatten(1, (4, 16)), "q") == 200
-    with pytest.raises(ValueError, match="heads of a row"):
-        rn._token_stride(torch.zeros(4, 16, 4).transpose(1, 2), "q")
-    with pytest.raises(ValueError, match="rows must not overlap"):
-        rn._token_stride(torch.zeros(1, 4, 16).expand(4, 4, 16), "q")
-    with pytest.raises(ValueError, match="shape mismatch"):
-        rn._packed_dims(q, k[:, :1], v, o, pool, 2)
-    with pytest.raises(ValueError, match="one dtype"):
-        rn._packed_dims(q, k, v, o.bfloat16(), pool, 2)
-    with pytest.raises(ValueError, match="pool"):
-        rn._packed_dims(q, k, v, o, pool.double(), 2)
-    with pytest.raises(ValueError, match="cu_seqlens"):
-        rn._index(cu.long(), torch.int32, 3, "cu_seqlens")
-    with pytest.raises(ValueError, match="slots"):
-        rn._index(sl, torch.int32, 3, "slots")
-    y = torch.zeros(3, 2, 8)
-    with pytest.raises(ValueError, match="one shape"):
-        rn._msr_args(y, (None, None), y[:, :, :4])
+    cases = [({}, "CUDA tensors"), (dict(q=wide[:, 3:67].unflatten(1, (4, 16))), "CUDA tensors"),
+             (dict(pos=None, theta=None), "CUDA tensors"), (dict(gamma=[0.9, 0.8]), "CUDA tensors"),
+             (dict(gamma=torch.full((2,), 0.9, dtype=torch.float64)), "CUDA tensors"),
+             (dict(q=torch.zeros(4, 16, 4).transpose(1, 2)), "heads of a row"),
+             (dict(q=torch.zeros(1, 4, 16).expand(4, 4, 16)), "rows must not overlap"),
+             (dict(k=k[:, :1]), "shape mismatch"), (dict(o=o[:3]), "shape mismatch"), (dict(q=q[0]), "three dimensions"),
+             (dict(o=o.bfloat16()), "one dtype"), (dict(pool=pool.double()), "pool"), (dict(pool=pool[:, :, :8]), "pool"),
+             (dict(pool=pool.transpose(2, 3)), "pool"), (dict(cu_seqlens=cu.long()), "cu_seqlens"),
+             (dict(cu_seqlens=cu[:2]), "cu_seqlens"), (dict(slots=sl[:, None]), "slots"), (dict(pos=pos.int()), "pos"),
+             (dict(gamma=G2[:1]), "gamma has 1 entries"), (dict(theta=TH8[:7]), "theta has 7 entries"),
+             (dict(workspace=torch.zeros(8, 8, dtype=torch.uint8).t()), "workspace")]
+    for change, why in cases:
+        with pytest.raises(ValueError, match=why):
+            rn.retnet_retention_packed(**{**good, **change})
+    step = {n: good[n] for n in ("q", "k", "v", "o", "pool", "gamma", "theta")}
+    step.update(slots=torch.zeros(4, dtype=torch.int32), pos=None)
+    for change, why in (({}, "CUDA tensors"), (dict(slots=sl), "slots"), (dict(pos=pos), "pos"), (dict(v=v[:2]), "shape mismatch")):
+        with pytest.raises(ValueError, match=why):
+            rn.retnet_retention_step_slots(**{**step, **change})
+    for args, why in (((pool, sl, sl), "CUDA tensors"), ((pool.double(), sl, sl), "float32"), ((pool, sl, sl[:1]), "dst"),
+                      ((pool, sl.long(), sl), "src"), ((pool.transpose(0, 1), sl, sl), "contiguous")):
+        with pytest.raises(ValueError, match=why):
+            rn.retnet_state_slots_copy(*args)
+    y, w = torch.zeros(3, 2, 8), torch.zeros(2, 8)
+    for args, why in (((y, y, w, w, y), "CUDA tensors"), ((y, y[:, :, :4], None, None, y), "one shape"),
+                      ((y, y.bfloat16(), None, None, y), "one shape"), ((y, y, torch.zeros(8), None, y), "float32"),
+                      ((y, y, w.double(), None, y), "float32"), ((y[0], y, None, None, y), "tokens"),
+                      ((y.transpose(0, 1), y, None, None, y), "contiguous")):
+        with pytest.raises(ValueError, match=why):
+            rn.retnet_msr_affine(*args)
+        with pytest.raises(ValueError, match=why):
+            rn.retnet_msr_affine_backward(*args, y, y)
+        with pytest.raises(ValueError, match=why):
+            rn.msr_affine_backward(*args)
     with pytest.raises(ValueError, match="float32"):
-        rn._msr_args(y, (torch.zeros(8), None), y)
+        rn.retnet_msr_affine_backward(y, y, w, w, y, y, y, torch.zeros(3, 8))
