@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kThreads) simt_scan_kernel(SimtPackedArgs<T> a
   const float lg = hp.log2g[h] * 0.693147180559945309f, full = expm1f(static_cast<float>(a.run) * lg);
   const int64_t step = static_cast<int64_t>(a.kv) * n;
   float* w = a.w + (u0 * a.kv + h) * n + e;
-  constexpr int kAhead = 4;
+  constexpr int kAhead = 8;
   for (int i0 = 0; i0 < first.runs; i0 += kAhead, w += kAhead * step) {
     float x[kAhead];
 #pragma unroll
@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(kThreads) simt_scan_kernel(SimtPackedArgs<T> a
 
 // grid (units x row tiles, heads, tiles of d_v)
 template <typename T>
-__global__ void __launch_bounds__(kThreads) simt_output_kernel(SimtPackedArgs<T> a, HeadParams hp) {
+__global__ void __launch_bounds__(kThreads, 3) simt_output_kernel(SimtPackedArgs<T> a, HeadParams hp) {
   __shared__ __align__(16) float as[kStep][kPitch], bs[kStep][kWidePitch];
   __shared__ __align__(16) float ps[kTile][kPitch];  // [key][row]
   pdl_wait();

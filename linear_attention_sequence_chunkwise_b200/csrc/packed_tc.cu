@@ -479,7 +479,7 @@ __global__ void __launch_bounds__(kScanThreads) tc_scan_kernel(TcPackedArgs a, H
   const float4* w = reinterpret_cast<const float4*>(a.w) + (u0 * a.kv + h) * n4 + e;
   uint2* r16 = reinterpret_cast<uint2*>(a.r16) + (u0 * a.kv + h) * n4 + e;
   float mx = 0.f;
-  constexpr int kAhead = 4;
+  constexpr int kAhead = 8;
   for (int i0 = 0; i0 < first.runs; i0 += kAhead) {
     float4 x[kAhead];
 #pragma unroll

@@ -30,11 +30,12 @@ struct StepSlotsArgs {
   const int64_t* pos;
   int64_t stride_q, stride_k, stride_v, stride_o;
   int32_t rows, n_slots, kv, group, d_k, d_v;
+  int32_t width;  // columns of a CTA, at most VEC * LANES: d_v in equal parts
   uint32_t flags;
 };
 
-// VEC: columns of a lane (4, or 1 where d_v or the pool allows no 16-byte access).  LANES: lanes that
-// cover the CTA's columns.  G: query heads of one pass over the state (the group, rounded up; a
+// VEC: columns of a lane (4, or 2 or 1 where d_v allows no wider access).  LANES: lanes that cover the
+// CTA's columns.  G: query heads of one pass over the state (the group, rounded up; a
 // larger group takes further passes that only read).
 template <typename T, int VEC, int LANES, int G>
 __global__ void __launch_bounds__(kThreads) step_slots_kernel(StepSlotsArgs<T> a, HeadParams hp) {
@@ -46,13 +47,14 @@ __global__ void __launch_bounds__(kThreads) step_slots_kernel(StepSlotsArgs<T> a
   float* qs = ks + dk;                    // [G][dk] rotated q of this pass
   float* red = qs + G * dk;               // [warps][G][kCols] partial q S
   __shared__ float factor;
-  const int row = blockIdx.x, h = blockIdx.y, c0 = blockIdx.z * kCols;
+  const int row = blockIdx.x, h = blockIdx.y, c0 = blockIdx.z * a.width;
+  const int c1 = c0 + a.width < dv ? c0 + a.width : dv;  // the CTA's columns end here
   const int32_t slot = a.slots[row];
   const int64_t pos = a.pos ? a.pos[row] : 0;
   if (slot < 0) return;  // padding
   const bool bad_row = slot >= a.n_slots || pos < 0;
   const int lr = tid / LANES, col = c0 + (tid % LANES) * VEC;
-  const bool live = col < dv;
+  const bool live = col < c1;
   const bool fresh = pos == 0;
   float* S = a.pool + (static_cast<int64_t>(bad_row ? 0 : slot) * a.kv + h) * dk * dv + col;
 
@@ -67,6 +69,9 @@ __global__ void __launch_bounds__(kThreads) step_slots_kernel(StepSlotsArgs<T> a
         if constexpr (VEC == 4) {
           const float4 x = __ldcs(reinterpret_cast<const float4*>(S + static_cast<int64_t>(i) * dv));
           st[u][0] = x.x; st[u][1] = x.y; st[u][2] = x.z; st[u][3] = x.w;
+        } else if constexpr (VEC == 2) {
+          const float2 x = __ldcs(reinterpret_cast<const float2*>(S + static_cast<int64_t>(i) * dv));
+          st[u][0] = x.x; st[u][1] = x.y;
         } else {
           st[u][0] = __ldcs(S + static_cast<int64_t>(i) * dv);
         }
@@ -109,7 +114,7 @@ __global__ void __launch_bounds__(kThreads) step_slots_kernel(StepSlotsArgs<T> a
   float vv[VEC];
 #pragma unroll
   for (int c = 0; c < VEC; ++c)
-    vv[c] = col + c < dv ? load_f(a.v + row * a.stride_v + static_cast<int64_t>(h) * dv, col + c) : 0.f;
+    vv[c] = col + c < c1 ? load_f(a.v + row * a.stride_v + static_cast<int64_t>(h) * dv, col + c) : 0.f;
   if (__syncthreads_or(dup | static_cast<int>(bad_row))) {
     if (tid == 0 && h == 0 && blockIdx.z == 0) atomicAdd(&g_step_errors, 1u);
     return;
@@ -150,6 +155,8 @@ __global__ void __launch_bounds__(kThreads) step_slots_kernel(StepSlotsArgs<T> a
             if constexpr (VEC == 4) {
               __stcs(reinterpret_cast<float4*>(S + static_cast<int64_t>(i) * dv),
                      make_float4(st[u][0], st[u][1], st[u][2], st[u][3]));
+            } else if constexpr (VEC == 2) {
+              __stcs(reinterpret_cast<float2*>(S + static_cast<int64_t>(i) * dv), make_float2(st[u][0], st[u][1]));
             } else {
               __stcs(S + static_cast<int64_t>(i) * dv, st[u][0]);
             }
@@ -180,7 +187,7 @@ __global__ void __launch_bounds__(kThreads) step_slots_kernel(StepSlotsArgs<T> a
     __syncthreads();
     for (int e = tid; e < G * kCols; e += kThreads) {
       const int g = e / kCols, c = e % kCols;
-      if (g0 + g < a.group && c0 + c < dv) {
+      if (g0 + g < a.group && c0 + c < c1) {
         float s = 0.f;
 #pragma unroll
         for (int w = 0; w < kThreads / 32; ++w) s += red[(w * G + g) * kCols + c];
@@ -196,8 +203,10 @@ cudaError_t launch_g(const PackedCall& c, const HeadParams& hp, cudaStream_t s) 
                      static_cast<T*>(c.o), c.pool, c.slot, c.pos, c.stride_q, c.stride_k, c.stride_v, c.stride_o,
                      static_cast<int32_t>(c.rows), static_cast<int32_t>(c.slots), static_cast<int32_t>(c.heads_kv),
                      static_cast<int32_t>(c.heads / c.heads_kv), static_cast<int32_t>(c.d_k),
-                     static_cast<int32_t>(c.d_v), c.flags};
+                     static_cast<int32_t>(c.d_v), 0, c.flags};
   constexpr int kCols = VEC * LANES;
+  const int64_t parts = (c.d_v + kCols - 1) / kCols;
+  a.width = static_cast<int32_t>(((c.d_v + parts - 1) / parts + VEC - 1) / VEC * VEC);
   // at most 4 * (9 * 512 + 8 * 8 * 128) = 51 KB
   const size_t smem = sizeof(float) * static_cast<size_t>((1 + G) * c.d_k + (kThreads / 32) * G * kCols);
   if (smem > 48 * 1024) {
@@ -206,7 +215,7 @@ cudaError_t launch_g(const PackedCall& c, const HeadParams& hp, cudaStream_t s) 
     if (e != cudaSuccess) return e;
   }
   const dim3 grid(static_cast<unsigned>(c.rows), static_cast<unsigned>(c.heads_kv),
-                  static_cast<unsigned>((c.d_v + kCols - 1) / kCols));
+                  static_cast<unsigned>(parts));
   step_slots_kernel<T, VEC, LANES, G><<<grid, kThreads, smem, s>>>(a, hp);
   return cudaGetLastError();
 }
@@ -222,7 +231,8 @@ cudaError_t launch_lanes(const PackedCall& c, const HeadParams& hp, cudaStream_t
 
 template <typename T>
 cudaError_t launch_typed(const PackedCall& c, const HeadParams& hp, cudaStream_t s) {
-  if (c.d_v % 4) return launch_lanes<T, 1, 32>(c, hp, s);
+  if (c.d_v % 2) return launch_lanes<T, 1, 32>(c, hp, s);
+  if (c.d_v % 4) return launch_lanes<T, 2, 32>(c, hp, s);
   // 128-column CTAs read 512-byte segments; where they are fewer than two an SM, 32-column ones
   if (c.rows * c.heads_kv * ((c.d_v + 127) / 128) < 296) return launch_lanes<T, 4, 8>(c, hp, s);
   return launch_lanes<T, 4, 32>(c, hp, s);
