@@ -53,9 +53,11 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PackedIndex ix, RunDesc*
   before = __reduce_add_sync(0xffffffffu, before);
   if (tid % 32 == 0 && before) atomicAdd(&total, before);
   bad = __syncthreads_or(bad);
-  if (rot.offset)  // its rows dealt out to the CTAs
-    for (int64_t r = u; r < 17; r += gridDim.x)
-      for (int j = tid; j < rot.half; j += kThreads) turn(rot.offset + r * 2 * rot.half + j / 4 * 8 + j % 4, rot, r, j, hp);
+  if (rot.offset)  // dealt out to the grid's threads
+    for (int64_t e = u * kThreads + tid; e < 17 * rot.half; e += static_cast<int64_t>(gridDim.x) * kThreads) {
+      const int r = static_cast<int>(e / rot.half), j = static_cast<int>(e % rot.half);
+      turn(rot.offset + r * 2 * rot.half + j / 4 * 8 + j % 4, rot, r, j, hp);
+    }
   const int s = total - 1;  // -1: the first sequence starts behind this unit
   if (bad || s < 0) {
     if (tid == 0) {

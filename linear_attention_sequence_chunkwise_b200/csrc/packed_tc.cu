@@ -315,7 +315,6 @@ __global__ void __launch_bounds__(StateCfg<M, NV>::kThreads, 1)
     float mx = 0.f;
     Two S[SEQ ? C::kHold / 2 : 1];
     float lg = 0.f, full_less = 0.f;
-    float* pool = nullptr;
     __half* r16 = nullptr;
     auto emit = [&](int64_t chunk) {  // the state before chunk `chunk`, rounded
       __half* to = r16 + chunk * state_size;
@@ -364,17 +363,54 @@ __global__ void __launch_bounds__(StateCfg<M, NV>::kThreads, 1)
 #pragma unroll
       for (int r = 0; r < 2 * kPer; ++r) decays[r] = decay_pow(lg, 127 - tr - r * kRows);
     };
+    // S from the pool, or to it, 128 columns at a time through shared memory (the small planes' place, free
+    // before the first step and behind the last), so that the pool is read and written in whole rows: a
+    // thread's own row, 16 bytes an access, took 4000 cycles each way.
+    auto exchange_pool = [&](bool out) {
+      constexpr int kPart = NV < 128 ? NV : 128, kChunks = kPart / 4;
+      unsigned char* tile = smem + (s2 - sm);
+      float* rows = a.pool + d0.slot * state_size + blockIdx.y * head_size + static_cast<int64_t>(k0) * a.d_v + v0;
+      const int my = row - k0, my_col = (warp / 4) * C::kHold;
+#pragma unroll
+      for (int p = 0; p < NV; p += kPart) {
+        const bool here = holds && my_col / kPart * kPart == p;
+        if (out && here) {
+#pragma unroll
+          for (int e = 0; e < C::kHold; e += 4) {
+            const float2 x = parts(S[SEQ ? e / 2 : 0]), y = parts(S[SEQ ? e / 2 + 1 : 0]);
+            const int c = (my_col - p + e) / 4;
+            *reinterpret_cast<float4*>(tile + (my * kChunks + (c ^ (my & 7))) * 16) = make_float4(x.x, x.y, y.x, y.y);
+          }
+        }
+        if (out) named_bar_sync(1, C::kData);
+#pragma unroll 8
+        for (int e = tid; e < M * kChunks; e += C::kData) {
+          const int r = e / kChunks, c = e % kChunks;
+          float4* at_pool = reinterpret_cast<float4*>(rows + static_cast<int64_t>(r) * a.d_v + p) + c;
+          float4* at_tile = reinterpret_cast<float4*>(tile + (r * kChunks + (c ^ (r & 7))) * 16);
+          if (out) *at_pool = *at_tile;
+          else *at_tile = *at_pool;
+        }
+        named_bar_sync(1, C::kData);
+        if (!out && here) {
+#pragma unroll
+          for (int e = 0; e < C::kHold; e += 4) {
+            const int c = (my_col - p + e) / 4;
+            const float4 x = *reinterpret_cast<const float4*>(tile + (my * kChunks + (c ^ (my & 7))) * 16);
+            S[SEQ ? e / 2 : 0] = two(x.x, x.y);
+            S[SEQ ? e / 2 + 1 : 0] = two(x.z, x.w);
+          }
+        }
+        if (!out) named_bar_sync(1, C::kData);
+      }
+    };
     if constexpr (SEQ) {
       set_head(blockIdx.y);
       full_less = decay_less_one(lg, kChunk);
-      pool = a.pool + d0.slot * state_size + blockIdx.y * head_size + static_cast<int64_t>(row) * a.d_v + cols;
       r16 = a.r16 + first * state_size + blockIdx.y * head_size + at;
 #pragma unroll
-      for (int e = 0; e < C::kHold; e += 4) {
-        const float4 x = d0.pos > 0 && holds ? *reinterpret_cast<const float4*>(pool + e) : make_float4(0.f, 0.f, 0.f, 0.f);
-        S[e / 2] = two(x.x, x.y);
-        S[e / 2 + 1] = two(x.z, x.w);
-      }
+      for (int e = 0; e < C::kHold / 2; ++e) S[e] = two(0.f);
+      if (d0.pos > 0) exchange_pool(false);
       if (d0.pos > 0) emit(0);
     }
     int n = 0, chunk = 0, last_step = -1;  // steps, chunks so far; the last step of the chunk before
@@ -435,15 +471,7 @@ __global__ void __launch_bounds__(StateCfg<M, NV>::kThreads, 1)
     if (alive && chunk > 0 && products_done(last_step)) {
       take(chunk - 1, SEQ ? decay_less_one(lg, last_tokens) : 0.f,
            SEQ ? exp2f(static_cast<float>(last_tokens - kChunk) * lg) : 1.f, last_unit, last_head);
-      if constexpr (SEQ) {
-        if (holds) {
-#pragma unroll
-          for (int e = 0; e < C::kHold; e += 4) {
-            const float2 x = parts(S[e / 2]), y = parts(S[e / 2 + 1]);
-            *reinterpret_cast<float4*>(pool + e) = make_float4(x.x, x.y, y.x, y.y);
-          }
-        }
-      }
+      if constexpr (SEQ) exchange_pool(true);
     }
     if constexpr (SEQ) report_fp16_range(mx);
   }
