@@ -48,11 +48,11 @@ struct TcPackedArgs {
   bool o_wide;  // rows of o start on 32-byte boundaries
 };
 
-// States in the workspace are [d_v / 8][d_k][8]: a thread that holds a row of d_k writes eight columns
-// at once beside its neighbours' (a row-major state cost 32 separate lines a store), and 64 columns of
-// fp16 are the un-swizzled operand of the tensor cores as they lie.
-__device__ __forceinline__ int64_t blocked(int row, int col, int d_k) {
-  return (static_cast<int64_t>(col / 8) * d_k + row) * 8 + col % 8;
+// States in the workspace are [d_k / M][d_v / 8][M][8], M = min(d_k, 128): a thread that holds a row of
+// d_k writes eight columns at once beside its neighbours' (a row-major state cost 32 separate lines a
+// store), and up to 128 columns of fp16 are the un-swizzled operand of the tensor cores as they lie.
+__device__ __forceinline__ int64_t blocked(int row, int col, int m, int d_v) {
+  return ((static_cast<int64_t>(row / m) * (d_v / 8) + col / 8) * m + row % m) * 8 + col % 8;
 }
 
 // Cosines and sines of four pairs, two and two.
@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(StateCfg<M, NV>::kThreads, 1)
     const int row = k0 + (M == 128 ? quarter * 32 + lane : quarter * 16 + lane % 16);
     const uint32_t t_mine = tm + (static_cast<uint32_t>(quarter * 32) << 16) + (warp / 4) * C::kHold;
     const int64_t head_size = static_cast<int64_t>(a.d_k) * a.d_v, state_size = a.kv * head_size;
-    const int64_t at = blocked(row, cols, a.d_k);
+    const int64_t at = blocked(row, cols, M, a.d_v);
     float mx = 0.f;
     Two S[SEQ ? C::kHold / 2 : 1];
     float lg = 0.f, full_less = 0.f;
@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(StateCfg<M, NV>::kThreads, 1)
           track(mx, x.x, x.y);
           w[j] = pack_f16x2(x.x, x.y);
         }
-        if (holds) *reinterpret_cast<uint4*>(to + static_cast<int64_t>(e) * a.d_k) = make_uint4(w[0], w[1], w[2], w[3]);
+        if (holds) *reinterpret_cast<uint4*>(to + e * M) = make_uint4(w[0], w[1], w[2], w[3]);
       }
     };
     // S <- S + less S + up D, D the products of the CTA's chunk-th chunk; or D to W of (unit, head)
@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(StateCfg<M, NV>::kThreads, 1)
             uint32_t x[8];
 #pragma unroll
             for (int m = 0; m < 8; ++m) x[m] = r[0][j + m];
-            st_global_v8(w + static_cast<int64_t>(e + j) * a.d_k, x);
+            st_global_v8(w + (e + j) * M, x);
           }
         }
       }
@@ -498,9 +498,10 @@ __global__ void __launch_bounds__(kScanThreads) tc_scan_kernel(TcPackedArgs a, H
   if (u0 < 0 || u0 >= a.units) return;  // cu_seqlens out of order: no run has tokens
   const RunDesc first = a.desc[u0];
   if (first.tokens == 0 || first.seq != s || e >= n4) return;
-  const int block = static_cast<int>(e / (2 * a.d_k)), in = static_cast<int>(e % (2 * a.d_k));  // (column block, half row)
+  const int m = a.d_k < 128 ? a.d_k : 128, block = static_cast<int>(e / (2 * m)), in = static_cast<int>(e % (2 * m));
+  const int row = block / (a.d_v / 8) * m + in / 2, col = block % (a.d_v / 8) * 8 + in % 2 * 4;
   float4* slot = reinterpret_cast<float4*>(a.pool + (static_cast<int64_t>(first.slot) * a.kv + h) * 4 * n4 +
-                                           static_cast<int64_t>(in / 2) * a.d_v + block * 8 + in % 2 * 4);
+                                           static_cast<int64_t>(row) * a.d_v + col);
   float4 r = first.pos > 0 ? *slot : make_float4(0.f, 0.f, 0.f, 0.f);
   const float lg = hp.log2g[h], full_less = decay_less_one(lg, kChunk);
   const int64_t step = static_cast<int64_t>(a.kv) * n4;
@@ -540,36 +541,37 @@ __global__ void __launch_bounds__(kScanThreads) tc_scan_kernel(TcPackedArgs a, H
 
 // ---- output ----------------------------------------------------------------------------------
 // CTA = (chunk, query head).  The data warps fetch q and k by asynchronous copies, rotate and round
-// them in place, turn the scores into bf16 pairs in tensor memory, and store the outputs: slice s
-// (64 columns of d_v) is the work of four of them, the others' slices run beside it.  One warp issues
-// all products (Q R + P V of a slice into the accumulator of its four warps), one fetches R (a bulk
-// copy: the workspace holds it as the tensor cores take it) and V through a ring whose last stage lies
-// over k, free after the scores.  When the data warps did all of this in turn, a slice cost 4800 cycles
-// (products 1800, copies 570, stores 1100, the rest barriers) at d_k 256.
+// them in place, turn the scores into bf16 pairs in tensor memory, and store the outputs: a slice of up
+// to 128 columns of d_v is the work of eight of them, the other eight's slice (d_k 256) runs beside it.
+// One warp issues all products (P V + Q R of a slice into the accumulator of its warps), one fetches V
+// and R in pieces of 32 KB through a ring whose last buffers lie over k, free after the scores.  V comes
+// by TMA, or in a sequence's last, shorter chunk by plain copies that leave zeros behind it; R by bulk
+// copies: the workspace holds it as the tensor cores take it.
+//   When the data warps did all of this in turn, a 64-column slice cost 4800 cycles at d_k 256; with the
+// issuing and copying warps 2300, bound by shared memory: a product of 64 columns reads as much of q as
+// one of 128, which is what the slices are now.
 template <int DK>
 struct OutCfg {
   static constexpr int kData = DK == 256 ? 512 : 256;
   static constexpr int kThreads = kData + 64;
-  static constexpr int NV = 64, kTeams = kData / 128;
-  static constexpr int kQ = kChunk * DK * 2;
-  static constexpr int kR = DK * NV * 2, kV = kChunk * NV * 2, kStage = kR + kV;
-  static constexpr int kOwn = DK == 128 ? 1 : 2;                 // ring stages besides k's area
-  static constexpr int kRing = kOwn + (kQ >= kStage ? 1 : 0);
-  static constexpr int kSmem = 2 * kQ + kOwn * kStage + 1024;
+  static constexpr int NV = 128, kTeams = kData / 256;            // teams of eight warps, an accumulator each
+  static constexpr int M = DK < 128 ? DK : 128;                   // rows of a piece of R
+  static constexpr int kQ = kChunk * DK * 2, kPiece = kChunk * NV * 2, kR = M * NV * 2;
+  static constexpr int kOwn = DK == 256 ? 3 : DK == 128 ? 1 : 2;  // buffers besides those in k's area
+  static constexpr int kRing = kOwn + kQ / kPiece;
+  static constexpr int kSmem = 2 * kQ + kOwn * kPiece + 1024;
   static constexpr int kCtas = kSmem <= 110 * 1024 ? 2 : 1;
   static constexpr int kCols = 128 + kTeams * NV <= 256 ? 256 : 512;  // S / P: 0..127, then the accumulators
-  // A slice is fetched again only when the one kRing before it is done, and its accumulator's next
-  // products wait for that fetch: no barrier runs two phases ahead of one who waits.
-  static_assert(kRing <= kTeams, "phases");
 };
 
 template <int DK>
-__global__ void __launch_bounds__(OutCfg<DK>::kThreads, OutCfg<DK>::kCtas) tc_output_kernel(TcPackedArgs a, HeadParams hp) {
+__global__ void __launch_bounds__(OutCfg<DK>::kThreads, OutCfg<DK>::kCtas)
+    tc_output_kernel(const __grid_constant__ CUtensorMap map_v, TcPackedArgs a, HeadParams hp) {
   using C = OutCfg<DK>;
   constexpr int NV = C::NV;
   extern __shared__ unsigned char raw_smem[];
-  // q and k ready; scores done; P ready; per ring stage: filled; per team: products done, read
-  __shared__ uint64_t bars[3 + C::kRing + 2 * C::kTeams];
+  // q and k ready; scores done; P ready; per buffer: filled, free; per team: products done, read
+  __shared__ uint64_t bars[3 + 2 * C::kRing + 2 * C::kTeams];
   __shared__ uint32_t tmem_at;
   __shared__ float factor[kChunk];
   // This grid starts when the state kernel before it has passed its own wait, so the plan is complete;
@@ -581,18 +583,19 @@ __global__ void __launch_bounds__(OutCfg<DK>::kThreads, OutCfg<DK>::kCtas) tc_ou
     return;
   }
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  const int hq = blockIdx.y, h = hq / a.group, slices = a.d_v / NV;
+  const int hq = blockIdx.y, h = hq / a.group, slices = (a.d_v + NV - 1) / NV;
   unsigned char* smem = raw_smem + ((1024u - (smem_addr(raw_smem) & 1023u)) & 1023u);
   const uint32_t sq = smem_addr(smem), sk = sq + C::kQ, own = sk + C::kQ;
-  const uint32_t b_qk = smem_addr(bars), b_s = b_qk + 8, b_p = b_qk + 16, b_full = b_qk + 24, b_done = b_full + 8 * C::kRing,
-                 b_read = b_done + 8 * C::kTeams;
+  const uint32_t b_qk = smem_addr(bars), b_s = b_qk + 8, b_p = b_qk + 16, b_full = b_qk + 24, b_free = b_full + 8 * C::kRing,
+                 b_done = b_free + 8 * C::kRing, b_read = b_done + 8 * C::kTeams;
   const bool has_r = !(d.index == 0 && d.pos == 0);
-  auto stage = [&](int s) -> uint32_t {
-    const int i = s % C::kRing;
-    return i < C::kOwn ? own + i * C::kStage : sk;
+  const int pieces = 1 + (has_r ? DK / C::M : 0);  // of a slice: V, then R by rows of M
+  auto buffer = [&](int n) -> uint32_t {  // of the n-th piece
+    const int i = n % C::kRing;
+    return i < C::kOwn ? own + i * C::kPiece : sk + (i - C::kOwn) * C::kPiece;
   };
+  auto columns = [&](int s) { return a.d_v - s * NV < NV ? a.d_v - s * NV : NV; };  // 64 or 128
   auto wait = [](uint32_t bar, int phase) { return mbar_wait(bar, phase & 1, kDrainBudget); };
-  auto done = [&](int s) { return wait(b_done + 8 * (s % C::kTeams), s / C::kTeams); };
   if (warp == 0) {
     tmem_alloc(smem_addr(&tmem_at), C::kCols);
     tmem_relinquish();
@@ -601,10 +604,10 @@ __global__ void __launch_bounds__(OutCfg<DK>::kThreads, OutCfg<DK>::kCtas) tc_ou
     mbar_init(b_qk, C::kData / 32);
     mbar_init(b_s, 1);
     mbar_init(b_p, C::kData / 32);
-    for (int i = 0; i < C::kRing; ++i) mbar_init(b_full + 8 * i, 2);
+    for (int i = 0; i < 2 * C::kRing; ++i) mbar_init(b_full + 8 * i, 1);
     for (int i = 0; i < C::kTeams; ++i) {
       mbar_init(b_done + 8 * i, 1);
-      mbar_init(b_read + 8 * i, 4);
+      mbar_init(b_read + 8 * i, 8);
     }
     fence_mbar_init();
   }
@@ -647,72 +650,80 @@ __global__ void __launch_bounds__(OutCfg<DK>::kThreads, OutCfg<DK>::kCtas) tc_ou
         mma_commit(b_s);
         ok = wait(b_p, 0);
       }
-      int s = 0;
+      int s = 0, n = 0;
       for (; ok && s < slices; ++s) {
         const int team = s % C::kTeams;
-        ok = wait(b_full + 8 * (s % C::kRing), s / C::kRing) && (s < C::kTeams || wait(b_read + 8 * team, s / C::kTeams - 1));
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t tO = tm + 128 + team * NV, at = stage(s);
-        const uint64_t dr = sdesc_cores(at, DK * 16, 128), dv = sdesc_sw128(at + C::kR, kBlock, 1024);
-        if (has_r) {
-          constexpr uint32_t ID = idesc_f16_f32(kChunk, NV, 0, 1);
+        const uint32_t tO = tm + 128 + team * NV;
+        const bool wide = columns(s) == NV;
+        if (!(ok = s < C::kTeams || wait(b_read + 8 * team, s / C::kTeams - 1))) break;
+        for (int p = 0; p < pieces; ++p, ++n) {
+          if (!(ok = wait(b_full + 8 * (n % C::kRing), n / C::kRing))) break;
+          tc_fence_after();
+          const uint32_t at = buffer(n);
+          if (p == 0) {
+            const uint32_t ID = wide ? idesc_bf16_f32(kChunk, NV, 0, 1) : idesc_bf16_f32(kChunk, 64, 0, 1);
+            const uint64_t dv = sdesc_sw128(at, kBlock, 1024);
 #pragma unroll
-          for (int ks = 0; ks < DK / 16; ++ks) mma_f16_ss(tO, dq + kstep(ks), dr + ((ks * 256) >> 4), ID, ks > 0);
+            for (int part = 1; part >= 0; --part)
+#pragma unroll
+              for (int ks = 0; ks < kChunk / 16; ++ks)
+                mma_f16_ts(tO, tS + (ks / 2) * 32 + part * 16 + (ks % 2) * 8, dv + ((ks * 2048) >> 4), ID, part == 0 || ks > 0);
+          } else {
+            const uint32_t ID = wide ? idesc_f16_f32(kChunk, NV, 0, 1) : idesc_f16_f32(kChunk, 64, 0, 1);
+            const uint64_t dr = sdesc_cores(at, C::M * 16, 128), da = dq + kstep((p - 1) * (C::M / 16));
+#pragma unroll
+            for (int ks = 0; ks < C::M / 16; ++ks) mma_f16_ss(tO, da + kstep(ks), dr + ((ks * 256) >> 4), ID, 1);
+          }
+          mma_commit(b_free + 8 * (n % C::kRing));
         }
-        constexpr uint32_t ID = idesc_bf16_f32(kChunk, NV, 0, 1);
-#pragma unroll
-        for (int part = 1; part >= 0; --part)
-#pragma unroll
-          for (int ks = 0; ks < kChunk / 16; ++ks)
-            mma_f16_ts(tO, tS + (ks / 2) * 32 + part * 16 + (ks % 2) * 8, dv + ((ks * 2048) >> 4), ID,
-                       has_r || part == 0 || ks > 0);
+        if (!ok) break;
         mma_commit(b_done + 8 * team);
       }
+      // nothing in flight when the tensor memory is freed
       wait(b_s, 0);
-      if (s > 0) done(s - 1);  // nothing in flight when the tensor memory is freed
+      for (int i = n > C::kRing ? n - C::kRing : 0; i < n; ++i) wait(b_free + 8 * (i % C::kRing), i / C::kRing);
+      if (s > 0) wait(b_done + 8 * ((s - 1) % C::kTeams), (s - 1) / C::kTeams);
     }
-  } else if (warp == C::kData / 32 + 1) {  // ---- R and V
-    const __nv_bfloat16* vp = a.v + static_cast<int64_t>(d.row) * a.stride_v + static_cast<int64_t>(h) * a.d_v +
-                              static_cast<int64_t>(lane / 8) * a.stride_v + lane % 8 * 8;
+  } else if (warp == C::kData / 32 + 1) {  // ---- V and R
+    const __nv_bfloat16* vp = a.v + static_cast<int64_t>(d.row) * a.stride_v + static_cast<int64_t>(h) * a.d_v;
     const __half* rp = a.r16 + (static_cast<int64_t>(blockIdx.x) * a.kv + h) * DK * a.d_v;
-    auto filled = [&](int s) {  // this warp's copies of slice s have landed
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(b_full + 8 * (s % C::kRing));
-    };
-    pdl_wait();
-    bool ok = true;
-    int s = 0;
-    for (; s < slices; ++s) {
-      if (s >= C::kRing) ok = done(s - C::kRing);
-      else if (s >= C::kOwn) ok = wait(b_s, 0);
-      if (!ok) break;
-      const uint32_t to = stage(s), bar = b_full + 8 * (s % C::kRing);
-      if (lane == 0) {
-        if (has_r) {
-          mbar_arrive_expect_tx(bar, C::kR);
-          bulk_load(to, rp + static_cast<int64_t>(s) * NV * DK, C::kR, bar);
-        } else {
-          mbar_arrive(bar);
+    bool ok = true, waited = false;
+    int n = 0;
+    for (int s = 0; ok && s < slices; ++s) {
+      for (int p = 0; p < pieces; ++p, ++n) {
+        const int i = n % C::kRing;
+        const uint32_t to = buffer(n), bar = b_full + 8 * i;
+        ok = n >= C::kRing ? wait(b_free + 8 * i, n / C::kRing - 1) : i < C::kOwn || wait(b_s, 0);
+        if (!ok) break;
+        if (p > 0) {
+          if (!waited) pdl_wait();
+          waited = true;
+          if (lane == 0) {
+            const uint32_t bytes = C::M * columns(s) * 2;
+            mbar_arrive_expect_tx(bar, bytes);
+            bulk_load(to, rp + (static_cast<int64_t>(p - 1) * a.d_v + s * NV) * C::M, bytes, bar);
+          }
+        } else if (d.tokens == kChunk) {
+          if (lane == 0) {
+            mbar_arrive_expect_tx(bar, C::kPiece);
+            tma_load_3d(to, &map_v, bar, 0, d.row, (h * a.d_v + s * NV) / 64);
+          }
+        } else {  // rows behind the sequence are zeros: 0 x v of another sequence may not be 0
+          const int chunks = columns(s) / 8;
+          for (int e = lane; e < kChunk * chunks; e += 32) {
+            const int r = e / chunks, c = e % chunks;
+            const bool in = r < d.tokens;
+            cp_async16(to + (c / 8) * kBlock + sw128(r, c % 8), vp + static_cast<int64_t>(in ? r : 0) * a.stride_v + s * NV + c * 8, in);
+          }
+          cp_async_wait_all();
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar);
         }
       }
-      const __nv_bfloat16* p = vp + s * NV;
-#pragma unroll
-      for (int i = 0; i < kChunk / 4; ++i) {
-        const int r = lane / 8 + 4 * i;
-        const bool in = r < d.tokens;
-        cp_async16(to + C::kR + sw128(r, lane % 8), p + static_cast<int64_t>(in ? 4 * i : 0) * a.stride_v - (in ? 0 : lane / 8 * a.stride_v), in);
-      }
-      cp_async_commit();
-      if (s > 0) {
-        cp_async_wait<1>();
-        filled(s - 1);
-      }
     }
-    cp_async_wait<0>();
-    if (s > 0) filled(s - 1);
-    for (int i = s > C::kRing ? s - C::kRing : 0; i < s; ++i) wait(b_full + 8 * (i % C::kRing), i / C::kRing);
+    if (!waited) pdl_wait();
+    for (int i = n > C::kRing ? n - C::kRing : 0; i < n; ++i) wait(b_full + 8 * (i % C::kRing), i / C::kRing);
   } else {  // ---- data
     const float lg = hp.log2g[h];
     constexpr int kBase = DK < 128 ? DK : 128;  // columns of a block of the rotations
@@ -754,13 +765,13 @@ __global__ void __launch_bounds__(OutCfg<DK>::kThreads, OutCfg<DK>::kCtas) tc_ou
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(b_qk);
-    const int quarter = warp % 4, row = quarter * 32 + lane, team = warp / 4;
+    const int quarter = warp % 4, row = quarter * 32 + lane, team = warp / 8;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     const float back = exp2f(-static_cast<float>(kChunk) * lg);
     if (wait(b_s, 0)) {
       tc_fence_after();
 #pragma unroll
-      for (int c = team * 32; c < kChunk; c += C::kTeams * 32) {
+      for (int c = (warp / 4) * 32; c < kChunk; c += C::kData / 4) {
         uint32_t r[2][16], p[2][16];
         tmem_ld_wait(tS + lanes + c, r);
         const int keep = c < quarter * 32 ? 31 : c > quarter * 32 ? -1 : lane;  // the row's last column here
@@ -778,21 +789,22 @@ __global__ void __launch_bounds__(OutCfg<DK>::kThreads, OutCfg<DK>::kCtas) tc_ou
       __syncwarp();
       if (lane == 0) mbar_arrive(b_p);
       const float f = factor[row];
-      __nv_bfloat16* op = a.o + (static_cast<int64_t>(d.row) + row) * a.stride_o + static_cast<int64_t>(hq) * a.d_v;
+      const int c0 = (warp / 4) % 2 * 64;  // this warp's columns of a slice
+      __nv_bfloat16* op = a.o + (static_cast<int64_t>(d.row) + row) * a.stride_o + static_cast<int64_t>(hq) * a.d_v + c0;
       const bool in = row < d.tokens, wide = a.o_wide;
       for (int s = team; s < slices; s += C::kTeams) {
-        if (!done(s)) break;
+        if (!wait(b_done + 8 * team, s / C::kTeams)) break;
         tc_fence_after();
 #pragma unroll
-        for (int c = 0; c < NV; c += 32) {
+        for (int c = 0; c < 64; c += 32) {
           uint32_t r[2][16];
-          tmem_ld_wait(tm + 128 + team * NV + lanes + c, r);
-          if (c + 32 == NV) {
+          tmem_ld_wait(tm + 128 + team * NV + lanes + c0 + c, r);
+          if (c == 32) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(b_read + 8 * team);
           }
-          if (!in) continue;
+          if (!in || c0 >= columns(s)) continue;
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             uint32_t w[8];
@@ -876,8 +888,10 @@ cudaError_t launch_shape(const PackedCall& c, const TcPackedArgs& a, const HeadP
                   : nv == 128 ? launch_states<M, 128, false>(c, a, hp, s) : launch_states<M, 64, false>(c, a, hp, s);
   }
   if (e != cudaSuccess) return e;
+  CUtensorMap mv;
+  if (!encode_token_rows(&mv, c.v, c.rows, c.heads_kv * c.d_v, c.stride_v, kChunk, 2)) return cudaErrorUnknown;
   return launch_dependent(tc_output_kernel<DK>, dim3(static_cast<unsigned>(a.units), static_cast<unsigned>(c.heads)),
-                          dim3(O::kThreads), O::kSmem, s, a, hp);
+                          dim3(O::kThreads), O::kSmem, s, mv, a, hp);
 }
 
 }  // namespace
