@@ -466,14 +466,27 @@ typedef struct {
  *   workspace: device, 16-byte aligned, at least retnet_packed_workspace_size bytes, in use until
  *   the call's work completes; two calls that share one must be ordered on the device.
  *   o and pool overlap no other argument.
- * The pool is updated in fp32.  A token whose q, k or v is not finite may make the outputs of up to
- * 255 earlier tokens of its own sequence not finite; it reaches no other sequence.
+ * Kernels: bf16 with d_k in {64, 128, 256}, d_v a multiple of 64, strides multiples of 8, 16-byte
+ * aligned q, k, v, o and gamma^128 >= 2^-12 for every head runs on the tensor cores (tcgen05), in
+ * chunks of 128 tokens; everything else, and RETNET_F_PRECISE, on the fp32 CUDA cores.
+ * retnet_packed_kernel tells which.
+ * Precision.  The pool is updated as in fp32 arithmetic on both (no bf16 input leaves a range).  The
+ * tensor-core outputs use fp16 copies of the rotated q and k and of the states before each chunk: they
+ * are finite for magnitudes below 65520, roundings outside are counted by retnet_fp16_range_errors.
+ * A token whose q, k or v is not finite may make the outputs of up to 255 earlier tokens of its own
+ * sequence not finite; it reaches no other sequence.
  */
 RETNET_API retnet_status_t retnet_retention_packed(const void* q, const void* k, const void* v, void* o,
                                         retnet_packed_t dims, retnet_dtype_t dtype, const float* gamma,
                                         const float* theta, uint32_t flags, const int32_t* cu_seqlens,
                                         const int32_t* slots, const int64_t* pos, float* pool,
                                         void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Which kernels a call of these dimensions runs on (host-only; assumes 16-byte aligned tensors): 1 = the
+ * tensor cores, 0 = the fp32 CUDA cores, negative = the negated status.  gamma: host float[heads_kv].
+ */
+RETNET_API int retnet_packed_kernel(retnet_packed_t dims, retnet_dtype_t dtype, uint32_t flags, const float* gamma);
 
 /* Workspace bytes of retnet_retention_packed (strides and slots are not read). */
 RETNET_API retnet_status_t retnet_packed_workspace_size(retnet_packed_t dims, size_t* bytes);

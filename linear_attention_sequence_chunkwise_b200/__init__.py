@@ -46,7 +46,7 @@ EXPORTS = ("retnet_retention_parallel", "retnet_retention_chunkwise", "retnet_re
            "retnet_backward_workspace_size", "retnet_backward_kernel", "retnet_backward_launches",
            "retnet_chunkwise_kernel", "retnet_chunkwise_launches", "retnet_debug_wait_timeouts",
            "retnet_fp16_range_errors", "retnet_debug_set_wait_budget",
-           "retnet_retention_packed", "retnet_packed_workspace_size", "retnet_retention_step_slots",
+           "retnet_retention_packed", "retnet_packed_kernel", "retnet_packed_workspace_size", "retnet_retention_step_slots",
            "retnet_state_slots_copy", "retnet_slot_errors", "retnet_msr_affine", "retnet_msr_affine_backward",
            "retnet_msr_affine_workspace_size", "retnet_status_string", "retnet_version")
 MAX_SLOT_PAIRS = 1024  # RETNET_MAX_SLOT_PAIRS
@@ -132,6 +132,7 @@ def load(path: str = None):
     _sz = ctypes.c_size_t
     lib.retnet_retention_packed.argtypes = [_vp, _vp, _vp, _vp, PackedDims, _i32, _vp, _vp, _u32, _vp, _vp, _vp, _vp,
                                             _vp, _sz, _vp]
+    lib.retnet_packed_kernel.argtypes = [PackedDims, _i32, _u32, _vp]
     lib.retnet_packed_workspace_size.argtypes = [PackedDims, ctypes.POINTER(_sz)]
     lib.retnet_retention_step_slots.argtypes = [_vp, _vp, _vp, _vp, PackedDims, _i32, _vp, _vp, _u32, _vp, _vp, _vp,
                                                 _vp]
@@ -141,7 +142,7 @@ def load(path: str = None):
     lib.retnet_msr_affine_backward.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64,
                                                ctypes.c_float, _i32, _vp, _sz, _vp]
     lib.retnet_msr_affine_workspace_size.argtypes = [_i64, _i64, _i64, ctypes.POINTER(_sz)]
-    for name in ("retnet_retention_packed", "retnet_packed_workspace_size", "retnet_retention_step_slots",
+    for name in ("retnet_retention_packed", "retnet_packed_kernel", "retnet_packed_workspace_size", "retnet_retention_step_slots",
                  "retnet_state_slots_copy", "retnet_slot_errors", "retnet_msr_affine", "retnet_msr_affine_backward",
                  "retnet_msr_affine_workspace_size"):
         getattr(lib, name).restype = _i32
@@ -495,6 +496,15 @@ def retnet_packed_workspace_size(dims) -> int:
     out = ctypes.c_size_t(0)
     _check(load().retnet_packed_workspace_size(PackedDims(*(int(x) for x in dims), 1), ctypes.byref(out)))
     return out.value
+
+
+def retnet_packed_kernel(dims, in_dtype, flags, gamma, strides=None):
+    """1 if retnet_retention_packed runs on the tensor cores for dims = (tokens, seqs, heads, heads_kv, d_k,
+    d_v), 0 for the CUDA cores, negative (-status) if it would be rejected; strides of q, k, v, o: dense."""
+    rows, seqs, heads, kv, dk, dv = (int(x) for x in dims)
+    d = PackedDims(rows, seqs, heads, kv, dk, dv, 1, *(strides or (heads * dk, kv * dk, kv * dv, heads * dv)))
+    g = _host_f32(gamma, kv)
+    return load().retnet_packed_kernel(d, int(in_dtype), int(flags), None if g is None else g.tobytes())
 
 
 def retnet_retention_packed(q, k, v, o, pool, cu_seqlens, slots, pos, gamma, theta=None,

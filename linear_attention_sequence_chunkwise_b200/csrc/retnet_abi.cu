@@ -570,6 +570,18 @@ PackedCall packed_call(const void* q, const void* k, const void* v, void* o, con
 }
 }  // namespace
 
+int retnet_packed_kernel(retnet_packed_t dims, retnet_dtype_t dtype, uint32_t flags, const float* gamma) {
+  retnet_status_t st = check_packed(dims, dtype, flags);
+  if (st != RETNET_OK) return -static_cast<int>(st);
+  HeadParams hp;
+  st = fill_params(&hp, gamma, nullptr, dims.heads_kv, dims.d_k, flags & ~static_cast<uint32_t>(RETNET_F_XPOS));
+  if (st != RETNET_OK) return -static_cast<int>(st);
+  return packed_tc_supported(packed_call(nullptr, nullptr, nullptr, nullptr, dims, dtype, flags, nullptr, nullptr, nullptr, nullptr),
+                             hp)
+             ? 1
+             : 0;
+}
+
 retnet_status_t retnet_packed_workspace_size(retnet_packed_t dims, size_t* bytes) {
   if (!bytes) return RETNET_ERR_NULL_PTR;
   if (dims.tokens < 0 || dims.seqs < 0 || dims.heads <= 0 || dims.heads_kv <= 0 || dims.d_k <= 0 || dims.d_v <= 0)

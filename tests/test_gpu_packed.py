@@ -37,9 +37,13 @@ def run(fused, pool, lens, slots, pos, gamma, theta, hq, kv, dk, dv, flags=FLAGS
     return o, p
 
 
-def check(lens, hq, kv, dk, dv, dtype, seed, flags=FLAGS, **kw):
+def check(lens, hq, kv, dk, dv, dtype, seed, flags=FLAGS, tensor_cores=None, **kw):
     fused, pool, slots, pos, gamma, theta = case(lens, hq, kv, dk, dv, dtype, seed, **kw)
     q, k, v = split(fused, hq, kv, dk, dv)
+    if tensor_cores is not None:
+        dims, width = (q.shape[0], len(lens), hq, kv, dk, dv), fused.shape[1]
+        kernel = rn.retnet_packed_kernel(dims, rn.BF16 if dtype == "bf16" else rn.F32, flags, gamma, (width,) * 3 + (hq * dv,))
+        assert kernel == int(tensor_cores)
     ref, after = reference(q, k, v, pool, lens, slots, pos, gamma, theta, flags)
     o, p = run(fused, pool, lens, slots, pos, gamma, theta, hq, kv, dk, dv, flags)
     eo, ep = errors(o, ref), errors(p, after)
@@ -60,7 +64,7 @@ LENS = [[1], [2, 1], [64, 63, 65], [128, 127, 129, 0, 1], [300], [256, 257, 255]
 @pytest.mark.parametrize("lens", LENS)
 @pytest.mark.parametrize("hq,kv,dk,dv,dtype", [(2, 2, 64, 64, "bf16"), (2, 1, 128, 128, "bf16"), (3, 3, 32, 40, "f32")])
 def test_lengths(lens, hq, kv, dk, dv, dtype):
-    check(lens, hq, kv, dk, dv, dtype, 100 + sum(lens))
+    check(lens, hq, kv, dk, dv, dtype, 100 + sum(lens), tensor_cores=dtype == "bf16")
 
 
 @pytest.mark.parametrize("hq,kv,dk,dv,dtype", [
@@ -71,7 +75,8 @@ def test_lengths(lens, hq, kv, dk, dv, dtype):
 ])
 def test_heads_and_widths(hq, kv, dk, dv, dtype):
     flags = FLAGS if dk % 2 == 0 else rn.F_SCALE_SQRT_D | rn.F_NORM_D
-    check([130, 1, 0, 300, 77], hq, kv, dk, dv, dtype, 7 * dk + dv, flags=flags)
+    check([130, 1, 0, 300, 77], hq, kv, dk, dv, dtype, 7 * dk + dv, flags=flags,
+          tensor_cores=dtype == "bf16" and dk in (64, 128, 256) and dv % 64 == 0)
 
 
 @pytest.mark.parametrize("flags", [0, rn.F_XPOS, rn.F_SCALE_SQRT_D, rn.F_NORM_D, FLAGS, FLAGS | rn.F_PRECISE])
@@ -84,6 +89,81 @@ def test_flags(flags, dtype):
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_decays(gamma, dtype):
     check([400, 257], 2, 2, 64, 64, dtype, 41, gamma=gamma)
+
+
+@pytest.mark.parametrize("lens,kv,dk,dv", [
+    ([700, 900], 1, 128, 128),           # few heads: states chunk by chunk, then the scan
+    ([700, 900], 1, 256, 256),           # two blocks of d_k
+    ([500, 1, 640, 0, 257], 24, 64, 64),  # many heads: a walk by sequence
+    ([300] * 7, 8, 128, 256),
+    ([1300], 2, 64, 320),                # 64 columns left over behind two slices of 128
+])
+def test_walks(lens, kv, dk, dv):
+    """Both walks over the states (by chunk, by sequence) at every block of d_k and slice of d_v."""
+    gamma = np.linspace(0.95, 0.9999, kv)  # (the schedule reaches 1 in fp32 at the 24th head)
+    check(lens, kv, kv, dk, dv, "bf16", dk + dv + len(lens), tensor_cores=True, gamma=gamma)
+
+
+@pytest.mark.parametrize("offset,pad", [(8, 0), (0, 8), (1, 0), (0, 4)])
+def test_alignments(offset, pad):
+    """Outputs and inputs off a 32-byte boundary (16-byte stores), and off a 16-byte one (CUDA cores)."""
+    lens, hq, kv, dk, dv = [200, 60], 2, 2, 64, 128
+    fused, pool, slots, pos, gamma, theta = case(lens, hq, kv, dk, dv, "bf16", 55)
+    ref, after = reference(*split(fused, hq, kv, dk, dv), pool, lens, slots, pos, gamma, theta, FLAGS)
+    rows, width = fused.shape
+
+    def place(t):
+        flat = torch.zeros(rows * (t.shape[1] + pad) + offset, dtype=t.dtype, device="cuda")
+        view = flat[offset:].view(rows, t.shape[1] + pad)[:, :t.shape[1]]
+        view.copy_(t)
+        return view
+    q, k, v = split(place(fused), hq, kv, dk, dv)
+    o = place(torch.zeros(rows, hq * dv, dtype=torch.bfloat16)).unflatten(1, (hq, dv))
+    p = pool.cuda()
+    rn.retnet_retention_packed(q, k, v, o, p, cu_of(lens).cuda(), torch.tensor(slots, dtype=torch.int32).cuda(),
+                               torch.tensor(pos).cuda(), gamma, theta)
+    torch.cuda.synchronize()
+    assert errors(o, ref) <= TOL_BF16 and errors(p, after) <= TOL_F32
+
+
+def test_fp16_range_is_counted():
+    """bf16 magnitudes beyond fp16's range: the outputs may be infinite and are counted; the states are not
+    affected, and neither is another sequence."""
+    lens, hq, kv, dk, dv = [150, 150], 2, 2, 64, 64
+    fused, pool, slots, pos, gamma, theta = case(lens, hq, kv, dk, dv, "bf16", 65, pos=[0, 3])
+    fused[20:40] *= 1e5
+    ref, after = reference(*split(fused, hq, kv, dk, dv), pool, lens, slots, pos, gamma, theta, FLAGS)
+    o, p = run(fused, pool, lens, slots, pos, gamma, theta, hq, kv, dk, dv)
+    assert rn.retnet_fp16_range_errors(clear=True) > 0
+    assert errors(o[150:300], ref[150:300]) <= TOL_BF16
+    for s in slots:
+        assert errors(p[s], after[s]) <= TOL_F32
+
+
+def test_two_calls_at_once():
+    """Two streams, each with its own workspace and slots, many times over: the same bits as one by one."""
+    args = []
+    for seed, lens, dk, dv in ((201, [300, 77, 513], 128, 128), (202, [64, 700], 64, 256)):
+        fused, pool, slots, pos, gamma, theta = case(lens, 4, 4, dk, dv, "bf16", seed)
+        args.append((fused, pool, lens, slots, pos, gamma, theta, 4, 4, dk, dv))
+    want = [run(*a) for a in args]
+    streams = [torch.cuda.Stream() for _ in args]
+    outs = []
+    for a, s in zip(args, streams):
+        fused, pool, lens, slots, pos, gamma, theta, hq, kv, dk, dv = a
+        q, k, v = split(fused.cuda(), hq, kv, dk, dv)
+        outs.append([(torch.full((q.shape[0], hq, dv), 0.25, dtype=q.dtype, device="cuda"), pool.cuda()) for _ in range(6)])
+        a += (q, k, v, cu_of(lens).cuda(), torch.tensor(slots, dtype=torch.int32).cuda(), torch.tensor(pos).cuda())
+        args[streams.index(s)] = a
+    torch.cuda.synchronize()
+    for i in range(6):
+        for a, s, o in zip(args, streams, outs):
+            q, k, v, cu, sl, ps = a[11:]
+            rn.retnet_retention_packed(q, k, v, o[i][0], o[i][1], cu, sl, ps, a[5], a[6], FLAGS, stream=s)
+    torch.cuda.synchronize()
+    for w, o in zip(want, outs):
+        for got in o:
+            assert torch.equal(w[0], got[0]) and torch.equal(w[1], got[1])
 
 
 def test_far_positions():
@@ -231,10 +311,10 @@ def test_matches_the_dense_call():
 def test_many_sequences():
     """More sequences than a plan's threads, lengths 0 to 9, and a pool past 2^31 bytes."""
     rng = np.random.default_rng(5)
-    lens = rng.integers(0, 10, 300).tolist()
+    lens = rng.integers(0, 10, 700).tolist()
     hq, kv, dk, dv = 2, 1, 64, 64
     n_slots = 140000  # 140000 * 16 KB = 2.3 GB
-    slots = (n_slots - 1 - rng.permutation(1000)[:300]).tolist()
+    slots = (n_slots - 1 - rng.permutation(1000)[:700]).tolist()
     fused, _, _, pos, gamma, theta = case(lens, hq, kv, dk, dv, "bf16", 131, slots=slots, n_slots=1)
     q, k, v = split(fused, hq, kv, dk, dv)
     small = si.randn((1000, kv, dk, dv), 132, "f32")

@@ -75,6 +75,20 @@ def test_packed_refusals(lib):
     assert _packed(lib, _dims(tokens=0), q=None) == 0 and _packed(lib, _dims(seqs=0), cu=None) == 0  # no work
 
 
+def test_packed_kernel_choice(lib):
+    f = rn.F_XPOS | rn.F_SCALE_SQRT_D | rn.F_NORM_D
+    g = np.array([1 - 2.0 ** -5, 0.999], np.float32)
+    def kern(dims=(300, 3, 4, 2, 128, 192), dtype=rn.BF16, flags=f, gamma=g, strides=None):
+        return rn.retnet_packed_kernel(dims, dtype, flags, gamma, strides)
+    assert kern() == 1 and kern((1, 1, 2, 2, 64, 64)) == 1 and kern((9, 2, 2, 2, 256, 512)) == 1
+    assert kern(dtype=rn.F32) == 0 and kern(flags=f | rn.F_PRECISE) == 0
+    assert kern((300, 3, 4, 2, 96, 192)) == 0 and kern((300, 3, 4, 2, 128, 200)) == 0
+    assert kern(gamma=np.array([0.93, 0.999], np.float32)) == 0  # 0.93^128 < 2^-12
+    assert kern(strides=(520, 256, 384, 768)) == 1 and kern(strides=(516, 256, 384, 768)) == 0
+    assert kern(dtype=7) == -3 and kern((300, 3, 3, 2, 128, 192)) == -2 and kern(flags=rn.F_NORM_R) == -5
+    assert kern(gamma=np.array([1.0, 0.9], np.float32)) == -4 and kern(gamma=None) == -1
+
+
 def test_step_refusals(lib):
     assert _step(lib, _dims(tokens=3)) == 2  # tokens != seqs
     assert _step(lib, dtype=5) == 3
