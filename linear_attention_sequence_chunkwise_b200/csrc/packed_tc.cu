@@ -178,7 +178,6 @@ __global__ void __launch_bounds__(StateCfg<M, NV>::kThreads, 1)
   __shared__ uint64_t bars[10];
   __shared__ uint32_t tmem_at;
   pdl_wait();
-  pdl_go();
   const int slices = a.d_v / NV;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int k0 = (blockIdx.z / slices) * M, v0 = (blockIdx.z % slices) * NV;
@@ -241,6 +240,7 @@ __global__ void __launch_bounds__(StateCfg<M, NV>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tm = tmem_at;
+  pdl_go();  // not before: an output CTA that took this one's tensor memory would wait for it for ever
   // n: steps of this CTA so far
   auto products_done = [&](int n) { return mbar_wait(b_done + 8 * (n & 1), (n >> 1) & 1, kDrainBudget); };
   auto filled = [&](int n) { return mbar_wait(b_full + 8 * (n % 3), (n / 3) & 1, kDrainBudget); };
@@ -574,7 +574,7 @@ __global__ void __launch_bounds__(OutCfg<DK>::kThreads, OutCfg<DK>::kCtas)
   __shared__ uint64_t bars[3 + 2 * C::kRing + 2 * C::kTeams];
   __shared__ uint32_t tmem_at;
   __shared__ float factor[kChunk];
-  // This grid starts when the state kernel before it has passed its own wait, so the plan is complete;
+  // This grid starts when every CTA of the kernel before it has passed its own wait, so the plan is complete;
   // it is read past the L1 cache.  The states are not: the copying warp waits before it fetches R (and
   // before the CTA ends, so that no later kernel runs beside the state kernel).
   const RunDesc d = plan_entry(a.desc + blockIdx.x);
