@@ -49,4 +49,17 @@ struct PackedRotation {
 cudaError_t launch_packed_plan(const PackedIndex& ix, RunDesc* desc, const PackedRotation& rot, const HeadParams& hp,
                                cudaStream_t s);
 
+// A state S decayed by gamma^n and added to: by S + (keep ? S : 0) + what is added.  Above 1/2 by is
+// gamma^n - 1 to full relative precision: the factor itself, near 1, would round the same way run after
+// run.  Below, gamma^n: there the sum with S would leave a rounding as large as the old state's behind.
+struct Decay {
+  float by;
+  bool keep;
+};
+__device__ __forceinline__ Decay decay_of(float log2g, int n) {
+  const float f = decay_pow(log2g, n);
+  if (f < 0.5f) return Decay{f, false};
+  return Decay{expm1f(static_cast<float>(n) * log2g * 0.693147180559945309f), true};
+}
+
 }  // namespace retnet

@@ -180,8 +180,8 @@ __global__ void __launch_bounds__(kThreads) simt_scan_kernel(SimtPackedArgs<T> a
   if (first.tokens == 0 || first.seq != s || e >= n) return;
   float* slot = a.pool + (static_cast<int64_t>(first.slot) * a.kv + h) * n + e;
   float r = first.pos > 0 ? *slot : 0.f;
-  // gamma^n - 1 keeps its accuracy where gamma^n, near 1, would round alike run after run
-  const float lg = hp.log2g[h] * 0.693147180559945309f, full = expm1f(static_cast<float>(a.run) * lg);
+  const float lg = hp.log2g[h];
+  const Decay full = decay_of(lg, a.run);
   const int64_t step = static_cast<int64_t>(a.kv) * n;
   float* w = a.w + (u0 * a.kv + h) * n + e;
   constexpr int kAhead = 8;
@@ -194,8 +194,8 @@ __global__ void __launch_bounds__(kThreads) simt_scan_kernel(SimtPackedArgs<T> a
     for (int i = 0; i < kAhead; ++i) {
       if (i0 + i >= first.runs) break;
       w[i * step] = r;
-      const float less = i0 + i + 1 < first.runs ? full : expm1f(static_cast<float>(a.desc[u0 + i0 + i].tokens) * lg);
-      r = fmaf(less, r, r + x[i]);
+      const Decay d = i0 + i + 1 < first.runs ? full : decay_of(lg, a.desc[u0 + i0 + i].tokens);
+      r = fmaf(d.by, r, (d.keep ? r : 0.f) + x[i]);
     }
   }
   *slot = r;

@@ -126,11 +126,6 @@ __device__ __forceinline__ void store_plane(unsigned char* to, Eight& y) {
   }
   *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
 }
-// gamma^n - 1 to full relative precision: a state decayed by fma(that, S, S) keeps the factor's
-// accuracy where the factor itself, near 1, would round the same way chunk after chunk.
-__device__ __forceinline__ float decay_less_one(float log2g, int n) {
-  return expm1f(static_cast<float>(n) * log2g * 0.693147180559945309f);
-}
 // Row factor s / c_p of §三.3 in fp32 (relative error of a few 2^-24; the output is bf16).
 __device__ __forceinline__ float row_factor32(float gamma, int d_k, int64_t p, uint32_t flags) {
   float f = (flags & RETNET_F_SCALE_SQRT_D) ? rsqrtf(static_cast<float>(d_k)) : 1.f;
@@ -314,7 +309,8 @@ __global__ void __launch_bounds__(StateCfg<M, NV>::kThreads, 1)
     const int64_t at = blocked(row, cols, M, a.d_v);
     float mx = 0.f;
     Two S[SEQ ? C::kHold / 2 : 1];
-    float lg = 0.f, full_less = 0.f;
+    float lg = 0.f;
+    Decay full{0.f, true};
     __half* r16 = nullptr;
     auto emit = [&](int64_t chunk) {  // the state before chunk `chunk`, rounded
       __half* to = r16 + chunk * state_size;
@@ -330,9 +326,10 @@ __global__ void __launch_bounds__(StateCfg<M, NV>::kThreads, 1)
         if (holds) *reinterpret_cast<uint4*>(to + e * M) = make_uint4(w[0], w[1], w[2], w[3]);
       }
     };
-    // S <- S + less S + up D, D the products of the CTA's chunk-th chunk; or D to W of (unit, head)
-    auto take = [&](int chunk, float less, float up, int64_t unit, int head) {
+    // S <- decay S + up D, D the products of the CTA's chunk-th chunk; or D to W of (unit, head)
+    auto take = [&](int chunk, Decay decay, float up, int64_t unit, int head) {
       tc_fence_after();
+      const Two kept = decay.keep ? ~0ull : 0ull;
       float* w = nullptr;
       if constexpr (!SEQ) w = a.w + (unit * a.kv + head) * head_size + at;
 #pragma unroll
@@ -343,7 +340,7 @@ __global__ void __launch_bounds__(StateCfg<M, NV>::kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             Two& x = S[e / 2 + j];
-            x = fma2(two(less), x, fma2(two(up), two(__uint_as_float(r[0][2 * j]), __uint_as_float(r[0][2 * j + 1])), x));
+            x = fma2(two(decay.by), x, fma2(two(up), two(__uint_as_float(r[0][2 * j]), __uint_as_float(r[0][2 * j + 1])), x & kept));
           }
         } else if (holds) {
 #pragma unroll
@@ -406,7 +403,7 @@ __global__ void __launch_bounds__(StateCfg<M, NV>::kThreads, 1)
     };
     if constexpr (SEQ) {
       set_head(blockIdx.y);
-      full_less = decay_less_one(lg, kChunk);
+      full = decay_of(lg, kChunk);
       r16 = a.r16 + first * state_size + blockIdx.y * head_size + at;
 #pragma unroll
       for (int e = 0; e < C::kHold / 2; ++e) S[e] = two(0.f);
@@ -459,7 +456,7 @@ __global__ void __launch_bounds__(StateCfg<M, NV>::kThreads, 1)
       if (!alive) break;
       if (chunk > 0) {  // its products ran beside this chunk's first steps
         if (!(alive = products_done(last_step))) break;
-        take(chunk - 1, full_less, 1.f, last_unit, last_head);
+        take(chunk - 1, full, 1.f, last_unit, last_head);
         if constexpr (SEQ) emit(i);
       }
       ++chunk;
@@ -469,7 +466,7 @@ __global__ void __launch_bounds__(StateCfg<M, NV>::kThreads, 1)
       last_tokens = it.tokens;
     }
     if (alive && chunk > 0 && products_done(last_step)) {
-      take(chunk - 1, SEQ ? decay_less_one(lg, last_tokens) : 0.f,
+      take(chunk - 1, SEQ ? decay_of(lg, last_tokens) : full,
            SEQ ? exp2f(static_cast<float>(last_tokens - kChunk) * lg) : 1.f, last_unit, last_head);
       if constexpr (SEQ) exchange_pool(true);
     }
@@ -503,7 +500,8 @@ __global__ void __launch_bounds__(kScanThreads) tc_scan_kernel(TcPackedArgs a, H
   float4* slot = reinterpret_cast<float4*>(a.pool + (static_cast<int64_t>(first.slot) * a.kv + h) * 4 * n4 +
                                            static_cast<int64_t>(row) * a.d_v + col);
   float4 r = first.pos > 0 ? *slot : make_float4(0.f, 0.f, 0.f, 0.f);
-  const float lg = hp.log2g[h], full_less = decay_less_one(lg, kChunk);
+  const float lg = hp.log2g[h];
+  const Decay full = decay_of(lg, kChunk);
   const int64_t step = static_cast<int64_t>(a.kv) * n4;
   const float4* w = reinterpret_cast<const float4*>(a.w) + (u0 * a.kv + h) * n4 + e;
   uint2* r16 = reinterpret_cast<uint2*>(a.r16) + (u0 * a.kv + h) * n4 + e;
@@ -523,16 +521,17 @@ __global__ void __launch_bounds__(kScanThreads) tc_scan_kernel(TcPackedArgs a, H
         track(mx, r.z, r.w);
         r16[u * step] = make_uint2(pack_f16x2(r.x, r.y), pack_f16x2(r.z, r.w));
       }
-      float less = full_less, up = 1.f;
+      Decay by = full;
+      float up = 1.f;
       if (u + 1 == first.runs) {
         const int len = a.desc[u0 + u].tokens;
-        less = decay_less_one(lg, len);
+        by = decay_of(lg, len);
         up = exp2f(static_cast<float>(len - kChunk) * lg);
       }
-      r.x = fmaf(less, r.x, fmaf(up, x[i].x, r.x));
-      r.y = fmaf(less, r.y, fmaf(up, x[i].y, r.y));
-      r.z = fmaf(less, r.z, fmaf(up, x[i].z, r.z));
-      r.w = fmaf(less, r.w, fmaf(up, x[i].w, r.w));
+      r.x = fmaf(by.by, r.x, fmaf(up, x[i].x, by.keep ? r.x : 0.f));
+      r.y = fmaf(by.by, r.y, fmaf(up, x[i].y, by.keep ? r.y : 0.f));
+      r.z = fmaf(by.by, r.z, fmaf(up, x[i].z, by.keep ? r.z : 0.f));
+      r.w = fmaf(by.by, r.w, fmaf(up, x[i].w, by.keep ? r.w : 0.f));
     }
   }
   *slot = r;

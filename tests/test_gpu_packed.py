@@ -327,3 +327,31 @@ def test_many_sequences():
     torch.cuda.synchronize()
     assert errors(o, ref) <= TOL_BF16 and errors(p[-1000:], after) <= TOL_F32
     assert not p[:-1000].any()
+
+
+@pytest.mark.parametrize("length,kv,dk,dv,dtype,gamma,run_of,start", [
+    (256, 1, 64, 64, "bf16", 0.94, 128, 0),    # tensor cores, a walk by sequence
+    (640, 1, 64, 64, "bf16", 0.94, 128, 70),   # chunk by chunk, then the scan
+    (240, 1, 64, 64, "bf16", 0.94, 128, 70),   # a short last chunk
+    (128, 2, 64, 64, "f32", 0.8, 64, 0),       # CUDA cores
+    (512, 1, 256, 128, "f32", 0.8, 256, 70),
+])
+def test_small_after_large(length, kv, dk, dv, dtype, gamma, run_of, start):
+    """A state that was 2^12 times larger a run ago leaves no rounding of that size behind: every entry
+    within 2e-5 of the decayed sum of magnitudes (128 fp32 additions of at most 2^-23 each, 1.5e-5, and
+    a few 1e-7 for the decay factors, exponents up to 12 in fp32)."""
+    fused, pool, slots, _, _, theta = case([length], kv, kv, dk, dv, dtype, length + dk, behind=0)
+    last = (length - 1) // run_of * run_of
+    fused[last - run_of:last, kv * dk:] *= 64.0  # k and v
+    g = np.full(kv, gamma, dtype=np.float32)
+    q, k, v = split(fused, kv, kv, dk, dv)
+    assert rn.retnet_packed_kernel((length, 1, kv, kv, dk, dv), rn.BF16 if dtype == "bf16" else rn.F32, 0, g) == (dtype == "bf16")
+    _, p = run(fused, pool, [length], slots, [start], g, theta, kv, kv, dk, dv, flags=0)
+    decay = g.astype(np.float64)[:, None] ** np.arange(length - 1, -1, -1)  # (kv, length)
+    k64, v64 = k.double().numpy(), v.double().numpy()
+    before = pool[slots[0]].double().numpy() * (g.astype(np.float64) ** length)[:, None, None] * (start > 0)
+    ref = np.einsum("ht,thi,thj->hij", decay, k64, v64) + before
+    size = np.einsum("ht,thi,thj->hij", decay, abs(k64), abs(v64)) + abs(before)
+    err = (abs(p[slots[0]].double().cpu().numpy() - ref) / size).max()
+    print(f"{err:.2e}")
+    assert err <= 2e-5
