@@ -440,9 +440,10 @@ RETNET_API retnet_status_t retnet_fp16_range_errors(unsigned int* count, int cle
  * slots, pos and cu_seqlens are DEVICE arrays, read by the kernels: a captured graph may be
  * replayed with other contents.  What they hold cannot be checked on the host; a sequence that they
  * name wrongly (a slot >= slots, a slot that an earlier sequence of the call with tokens has, a
- * negative position) is left out: its rows of o and the pool stay as they were, and
- * retnet_slot_errors counts it.  A sequence with slot < 0 is padding: left out and not counted.
+ * position below 0 or above RETNET_MAX_POSITION) is left out: its rows of o and the pool stay as they
+ * were, and retnet_slot_errors counts it.  A sequence with slot < 0 is padding: left out and not counted.
  */
+#define RETNET_MAX_POSITION (1LL << 52) /* of a sequence's first token in a call: angles stay exact in fp64 */
 typedef struct {
     int64_t tokens;   /* rows of q, k, v, o */
     int64_t seqs;     /* sequences: entries of slots and pos; at most 65535 */
@@ -471,8 +472,10 @@ typedef struct {
  * chunks of 128 tokens; everything else, and RETNET_F_PRECISE, on the fp32 CUDA cores.
  * retnet_packed_kernel tells which.
  * Precision.  The pool is updated as in fp32 arithmetic on both (no bf16 input leaves a range).  The
- * tensor-core outputs use fp16 copies of the rotated q and k and of the states before each chunk: they
- * are finite for magnitudes below 65520, roundings outside are counted by retnet_fp16_range_errors.
+ * tensor-core outputs use fp16 copies of the rotated q and k, q decayed by up to gamma^128, k by up to
+ * gamma^127, and of the states before each chunk: 2^-11 of the value, but no finer than 2^-25 (below a
+ * magnitude of 2^-14 the relative accuracy falls), and finite below 65520; roundings outside are counted by
+ * retnet_fp16_range_errors.  RETNET_F_PRECISE has neither limit.
  * A token whose q, k or v is not finite may make the outputs of up to 255 earlier tokens of its own
  * sequence not finite; it reaches no other sequence.
  */

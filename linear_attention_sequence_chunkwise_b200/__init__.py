@@ -50,6 +50,7 @@ EXPORTS = ("retnet_retention_parallel", "retnet_retention_chunkwise", "retnet_re
            "retnet_state_slots_copy", "retnet_slot_errors", "retnet_msr_affine", "retnet_msr_affine_backward",
            "retnet_msr_affine_workspace_size", "retnet_status_string", "retnet_version")
 MAX_SLOT_PAIRS = 1024  # RETNET_MAX_SLOT_PAIRS
+MAX_POSITION = 2 ** 52  # RETNET_MAX_POSITION
 
 
 class RetnetError(RuntimeError):

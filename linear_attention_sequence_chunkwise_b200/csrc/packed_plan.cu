@@ -22,7 +22,7 @@ __device__ __forceinline__ void turn(float* row, const PackedRotation& rot, int6
 // One CTA a unit.  The sequence of a unit is the last one whose first unit is not behind it.  A call
 // whose cu_seqlens is out of order or leaves the rows has no runs; a sequence is refused (no run)
 // when its slot is out of range or an earlier sequence with tokens has it, or its position is
-// negative; one with slot < 0 or no tokens has none either.  Bound by the latency of its few
+// out of range; one with slot < 0 or no tokens has none either.  Bound by the latency of its few
 // dependent steps: the arrays of up to kThreads sequences are fetched at once and the rest is done
 // from shared memory.
 __global__ void __launch_bounds__(kThreads) plan_kernel(PackedIndex ix, RunDesc* __restrict__ desc, PackedRotation rot,
@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PackedIndex ix, RunDesc*
     dup |= cached ? slots[j] == slot && cu[j + 1] > cu[j] : ix.slots[j] == slot && ix.cu[j + 1] > ix.cu[j];
   dup = __syncthreads_or(dup);
   const int64_t i = u - (a / ix.run + s), runs = (len + ix.run - 1) / ix.run, left = len - i * ix.run;
-  const bool wanted = i < runs && slot >= 0, refused = dup || slot >= ix.n_slots || pos < 0;
+  const bool wanted = i < runs && slot >= 0, refused = dup || slot >= ix.n_slots || pos < 0 || pos > RETNET_MAX_POSITION;
   const bool live = wanted && !refused;
   if (tid == 0) {
     if (wanted && refused && i == 0) atomicAdd(&g_packed_errors, 1u);

@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(kThreads) step_slots_kernel(StepSlotsArgs<T> a
   const int32_t slot = a.slots[row];
   const int64_t pos = a.pos ? a.pos[row] : 0;
   if (slot < 0) return;  // padding
-  const bool bad_row = slot >= a.n_slots || pos < 0;
+  const bool bad_row = slot >= a.n_slots || pos < 0 || pos > RETNET_MAX_POSITION;
   const int lr = tid / LANES, col = c0 + (tid % LANES) * VEC;
   const bool live = col < c1;
   const bool fresh = pos == 0;

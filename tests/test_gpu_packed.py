@@ -355,3 +355,20 @@ def test_small_after_large(length, kv, dk, dv, dtype, gamma, run_of, start):
     err = (abs(p[slots[0]].double().cpu().numpy() - ref) / size).max()
     print(f"{err:.2e}")
     assert err <= 2e-5
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_positions_up_to_the_limit(dtype):
+    """The largest position is computed (frequencies that are powers of two: exact angles in the
+    reference); one more is left out and counted."""
+    lens, hq, kv, dk, dv = [150, 20, 1], 2, 2, 64, 64
+    theta = (2.0 ** -np.arange(dk // 2)).astype(np.float32)
+    fused, pool, slots, _, gamma, _ = case(lens, hq, kv, dk, dv, dtype, 111)
+    q, k, v = split(fused, hq, kv, dk, dv)
+    used = [slots[0], -1, slots[2]]
+    pos = [rn.MAX_POSITION, rn.MAX_POSITION + 1, rn.MAX_POSITION]
+    ref, after = reference(q, k, v, pool, lens, used, pos, gamma, theta, FLAGS)
+    o, p = run(fused, pool, lens, slots, pos, gamma, theta, hq, kv, dk, dv)
+    assert rn.retnet_slot_errors(clear=True) == 1
+    assert errors(o, ref) <= (TOL_BF16 if dtype == "bf16" else TOL_F32) and errors(p, after) <= TOL_F32
+    assert bool((o[150:170] == 0.25).all()) and torch.equal(p[slots[1]].cpu(), pool[slots[1]])

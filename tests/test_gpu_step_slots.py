@@ -78,6 +78,18 @@ def test_step_without_positions_and_at_far_ones():
         assert errors(o, ref) <= TOL_F32 and errors(p, after) <= TOL_F32
 
 
+def test_step_positions_up_to_the_limit():
+    hq, kv, dk, dv = 2, 2, 64, 64
+    theta = (2.0 ** -np.arange(dk // 2)).astype(np.float32)  # exact angles in the reference
+    fused, pool, slots, _, gamma, _ = case([1] * 3, hq, kv, dk, dv, "f32", 9, behind=0)
+    q, k, v = split(fused, hq, kv, dk, dv)
+    pos = [rn.MAX_POSITION, rn.MAX_POSITION + 1, 3]
+    ref, after = reference(q, k, v, pool, [1] * 3, [slots[0], -1, slots[2]], pos, gamma, theta, FLAGS)
+    o, p = step(fused, pool, slots, pos, gamma, theta, hq, kv, dk, dv)
+    assert rn.retnet_slot_errors(clear=True) == 1
+    assert errors(o, ref) <= TOL_F32 and errors(p, after) <= TOL_F32 and bool((o[1] == 0.25).all())
+
+
 def test_pool_past_32_bit_offsets():
     """Slots behind 2^31 floats (8.6 GB) are reached by the step and by the copy."""
     kv, dk, dv = 1, 256, 512
