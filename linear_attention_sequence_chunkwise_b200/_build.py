@@ -48,7 +48,7 @@ def _binding_command(out):
     return ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-w",
             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-DTORCH_EXTENSION_NAME=_torch_binding",
             *[f"-I{d}" for d in includes], BINDING_SRC, "-o", out, f"-L{os.path.join(root, 'lib')}", "-lc10", "-lc10_cuda",
-            "-ltorch_cpu", "-ltorch", "-ltorch_python", f"-L{PKG}", "-l:libretnet.so", "-Wl,-rpath,$ORIGIN"]
+            "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-ltorch_python", f"-L{PKG}", "-l:libretnet.so", "-Wl,-rpath,$ORIGIN"]
 
 
 def _build_binding():

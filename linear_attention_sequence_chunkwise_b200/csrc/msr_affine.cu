@@ -187,12 +187,13 @@ __device__ __forceinline__ void load_affine(Two (&w)[MG][4], Two (&b)[MG][4], co
 // grid (blocks, heads): the CTA's rows are tokens blockIdx.x * rows + i, + gridDim.x * rows, ...
 template <typename T, int MG, int W, int LPR, bool FULL>
 __global__ void __launch_bounds__(kThreads, MG == 1 ? 4 : 1)
-    msr_affine_kernel(const T* y, const T* g, const float* __restrict__ weight, const float* __restrict__ bias, T* out,
+    msr_affine_kernel(const T* y, const T* g, const float* weight, const float* bias, T* out,
                       int64_t tokens, int heads, int d_v, float eps) {
   constexpr int kRows = kThreads / LPR;
   const int lane = threadIdx.x % LPR, h = blockIdx.y;
   const float inv_n = 1.f / static_cast<float>(d_v);
   Two w[MG][4], b[MG][4];
+  pdl_wait();
   load_affine<MG, W, LPR>(w, b, weight, bias, h, lane, d_v);
   const int64_t step = static_cast<int64_t>(gridDim.x) * kRows, pitch = static_cast<int64_t>(heads) * d_v;
   const int64_t first = static_cast<int64_t>(blockIdx.x) * kRows;
@@ -233,14 +234,14 @@ __global__ void __launch_bounds__(kThreads, MG == 1 ? 4 : 1)
 // grid (blocks, heads).  part: [blocks][2][heads][d_v], dw then db.
 template <typename T, int MG, int W, int LPR, bool FULL>
 __global__ void __launch_bounds__(kThreads, MG == 1 ? 2 : 1)
-    msr_backward_kernel(const T* __restrict__ y, const T* __restrict__ g, const T* __restrict__ dout,
-                        const float* __restrict__ weight, const float* __restrict__ bias, T* __restrict__ dy,
-                        T* __restrict__ dg, float* __restrict__ part, int64_t tokens, int heads, int d_v, float eps) {
+    msr_backward_kernel(const T* y, const T* g, const T* dout, const float* weight, const float* bias, T* dy, T* dg,
+                        float* part, int64_t tokens, int heads, int d_v, float eps) {
   extern __shared__ float red[];  // [rows][d_v]
   constexpr int kRows = kThreads / LPR;
   const int lane = threadIdx.x % LPR, row = threadIdx.x / LPR, h = blockIdx.y;
   const float inv_n = 1.f / static_cast<float>(d_v);
   Two w[MG][4], b[MG][4], dw[MG][4], db[MG][4];
+  pdl_wait();
   load_affine<MG, W, LPR>(w, b, weight, bias, h, lane, d_v);
 #pragma unroll
   for (int m = 0; m < MG; ++m)
@@ -383,10 +384,9 @@ struct Forward {
   template <typename T, int MG, int W, int LPR, bool FULL>
   cudaError_t run() {
     const dim3 grid(static_cast<unsigned>(blocks_of(c.tokens, c.heads, kThreads / LPR, 4)), static_cast<unsigned>(c.heads));
-    msr_affine_kernel<T, MG, W, LPR, FULL><<<grid, kThreads, 0, s>>>(
-        static_cast<const T*>(c.y), static_cast<const T*>(c.g), c.weight, c.bias, static_cast<T*>(out), c.tokens,
-        static_cast<int>(c.heads), static_cast<int>(c.d_v), c.eps);
-    return cudaGetLastError();
+    return launch_dependent(msr_affine_kernel<T, MG, W, LPR, FULL>, grid, dim3(kThreads), 0, s, static_cast<const T*>(c.y),
+                            static_cast<const T*>(c.g), c.weight, c.bias, static_cast<T*>(out), c.tokens,
+                            static_cast<int>(c.heads), static_cast<int>(c.d_v), c.eps);
   }
 };
 struct Backward {
@@ -401,10 +401,10 @@ struct Backward {
     const dim3 grid(static_cast<unsigned>(backward_blocks(c.tokens, c.heads, c.d_v)), static_cast<unsigned>(c.heads));
     // at most 32 KB: kThreads / LPR rows of at most 8 LPR (LPR < 32) or 1024 values
     const size_t smem = part ? sizeof(float) * (kThreads / LPR) * static_cast<size_t>(c.d_v) : 0;
-    msr_backward_kernel<T, MG, W, LPR, FULL><<<grid, kThreads, smem, s>>>(
-        static_cast<const T*>(c.y), static_cast<const T*>(c.g), static_cast<const T*>(dout), c.weight, c.bias,
-        static_cast<T*>(dy), static_cast<T*>(dg), part, c.tokens, static_cast<int>(c.heads), static_cast<int>(c.d_v), c.eps);
-    return cudaGetLastError();
+    return launch_dependent(msr_backward_kernel<T, MG, W, LPR, FULL>, grid, dim3(kThreads), smem, s,
+                            static_cast<const T*>(c.y), static_cast<const T*>(c.g), static_cast<const T*>(dout), c.weight,
+                            c.bias, static_cast<T*>(dy), static_cast<T*>(dg), part, c.tokens, static_cast<int>(c.heads),
+                            static_cast<int>(c.d_v), c.eps);
   }
 };
 template <typename T, int W, int MG, int LPR, typename F>

@@ -25,13 +25,14 @@ __device__ __forceinline__ void turn(float* row, const PackedRotation& rot, int6
 // out of range; one with slot < 0 or no tokens has none either.  Bound by the latency of its few
 // dependent steps: the arrays of up to kThreads sequences are fetched at once and the rest is done
 // from shared memory.
-__global__ void __launch_bounds__(kThreads) plan_kernel(PackedIndex ix, RunDesc* __restrict__ desc, PackedRotation rot,
+__global__ void __launch_bounds__(kThreads) plan_kernel(PackedIndex ix, RunDesc* desc, PackedRotation rot,
                                                         HeadParams hp) {
   __shared__ int32_t cu[kThreads + 1], slots[kThreads];
   __shared__ int64_t poss[kThreads];
   __shared__ int total;
   const int tid = threadIdx.x;
   const int64_t u = blockIdx.x;
+  pdl_wait();
   pdl_go();
   if (tid == 0) total = 0;
   int bad = 0, before = 0;
@@ -96,8 +97,8 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PackedIndex ix, RunDesc*
 
 cudaError_t launch_packed_plan(const PackedIndex& ix, RunDesc* desc, const PackedRotation& rot, const HeadParams& hp,
                                cudaStream_t s) {
-  plan_kernel<<<static_cast<unsigned>(packed_units(ix.rows, ix.seqs, ix.run)), kThreads, 0, s>>>(ix, desc, rot, hp);
-  return cudaGetLastError();
+  return launch_dependent(plan_kernel, dim3(static_cast<unsigned>(packed_units(ix.rows, ix.seqs, ix.run))), dim3(kThreads), 0, s,
+                          ix, desc, rot, hp);
 }
 
 cudaError_t packed_index_errors(unsigned int* count, bool clear) {

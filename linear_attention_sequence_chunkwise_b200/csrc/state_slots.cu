@@ -11,6 +11,7 @@
 // asynchronous copies, 64 KB at once, two CTAs an SM, one storing while the other loads.  Otherwise it
 // streams through registers.
 #include "launch.h"
+#include "pdl.cuh"
 #include "sm100_ptx.cuh"
 
 namespace retnet {
@@ -34,14 +35,14 @@ __device__ __forceinline__ float4 zero_of<float4>() { return make_float4(0.f, 0.
 // power of two.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) slots_copy_kernel(T* pool, int32_t n_slots, int64_t n_cols, int log_cols,
-                                                              const int32_t* __restrict__ src,
-                                                              const int32_t* __restrict__ dst, int n) {
+                                                              const int32_t* src, const int32_t* dst, int n) {
   extern __shared__ __align__(16) unsigned char stage_raw[];
   T* stage = reinterpret_cast<T*>(stage_raw);
   __shared__ int32_t raw_dst[kMaxPairs], sp[kMaxPairs], dp[kMaxPairs];
   __shared__ int count;
   const int tid = threadIdx.x;
   if (tid == 0) count = 0;
+  pdl_wait();
   for (int i = tid; i < n; i += kThreads) raw_dst[i] = dst[i];
   __syncthreads();
   // The pairs to move, in any order (their destinations differ).  A pair with dst < 0 is padding;
@@ -133,9 +134,9 @@ cudaError_t launch_typed(float* pool, int64_t slots, int64_t slot_floats, const 
   while (static_cast<size_t>(2 << log_cols) * sizeof(T) * n <= kStageBytes && (n_cols >> (log_cols + 1)) >= 2 * sms) ++log_cols;
   const int64_t tiles = (n_cols + (1 << log_cols) - 1) >> log_cols;
   const int64_t blocks = tiles < 2 * sms ? tiles : 2 * sms;
-  slots_copy_kernel<T><<<static_cast<unsigned>(blocks), kThreads, (static_cast<size_t>(n) << log_cols) * sizeof(T), s>>>(
-      reinterpret_cast<T*>(pool), static_cast<int32_t>(slots), n_cols, log_cols, src, dst, static_cast<int>(n));
-  return cudaGetLastError();
+  return launch_dependent(slots_copy_kernel<T>, dim3(static_cast<unsigned>(blocks)), dim3(kThreads),
+                          (static_cast<size_t>(n) << log_cols) * sizeof(T), s, reinterpret_cast<T*>(pool),
+                          static_cast<int32_t>(slots), n_cols, log_cols, src, dst, static_cast<int>(n));
 }
 
 }  // namespace

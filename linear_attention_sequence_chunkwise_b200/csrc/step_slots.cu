@@ -10,6 +10,7 @@
 // loaded before the rotation is computed and the row's slot is checked against the others', so that
 // latency is paid once.
 #include "launch.h"
+#include "pdl.cuh"
 
 namespace retnet {
 namespace {
@@ -49,6 +50,7 @@ __global__ void __launch_bounds__(kThreads) step_slots_kernel(StepSlotsArgs<T> a
   __shared__ float factor;
   const int row = blockIdx.x, h = blockIdx.y, c0 = blockIdx.z * a.width;
   const int c1 = c0 + a.width < dv ? c0 + a.width : dv;  // the CTA's columns end here
+  pdl_wait();
   const int32_t slot = a.slots[row];
   const int64_t pos = a.pos ? a.pos[row] : 0;
   if (slot < 0) return;  // padding
@@ -216,8 +218,7 @@ cudaError_t launch_g(const PackedCall& c, const HeadParams& hp, cudaStream_t s) 
   }
   const dim3 grid(static_cast<unsigned>(c.rows), static_cast<unsigned>(c.heads_kv),
                   static_cast<unsigned>(parts));
-  step_slots_kernel<T, VEC, LANES, G><<<grid, kThreads, smem, s>>>(a, hp);
-  return cudaGetLastError();
+  return launch_dependent(step_slots_kernel<T, VEC, LANES, G>, grid, dim3(kThreads), smem, s, a, hp);
 }
 
 template <typename T, int VEC, int LANES>

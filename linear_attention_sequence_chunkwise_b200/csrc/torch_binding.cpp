@@ -5,8 +5,7 @@
 // same checks and ctypes marshalling in Python took 9 us beside a 4 us kernel, here they take about 1.
 // Argument errors are ValueErrors; the library's status is returned.
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
-#include <ATen/ops/empty_like.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <pybind11/numpy.h>
@@ -60,8 +59,12 @@ class Place {
     if (stream_) guard.emplace(c10::cuda::getStreamFromExternal(reinterpret_cast<cudaStream_t>(*stream_), device_.index()));
     return fn();
   }
+  // A new contiguous tensor, past the dispatcher (0.4 us less a tensor).
+  Tensor fresh(at::IntArrayRef sizes, at::ScalarType type) const {
+    return Tensor(at::detail::empty_cuda(sizes, type, device_, std::nullopt));
+  }
   Tensor bytes(size_t n) const {
-    return allocate([&] { return at::empty({static_cast<int64_t>(n)}, at::TensorOptions().dtype(at::kByte).device(device_)); });
+    return allocate([&] { return fresh({static_cast<int64_t>(n)}, at::kByte); });
   }
 
  private:
@@ -189,7 +192,7 @@ std::tuple<int, Tensor> msr_affine_new(const Tensor& y, const Tensor& g, const M
                                        const Stream& stream) {
   check_msr(y, {&g}, {&weight, &bias});
   const Place place(y, {&g, address(weight), address(bias)}, stream);
-  const Tensor out = place.allocate([&] { return at::empty_like(y); });
+  const Tensor out = place.allocate([&] { return place.fresh(y.sizes(), y.scalar_type()); });
   return {run_msr_affine(place, y, g, weight, bias, out, eps), out};
 }
 
@@ -225,10 +228,9 @@ std::tuple<int, Tensor, Tensor, Tensor, Tensor> msr_affine_backward_new(const Te
                                                                         const Maybe& workspace, const Stream& stream) {
   check_msr(y, {&g, &dout}, {&weight, &bias});
   const Place place(y, {&g, &dout, address(weight), address(bias), address(workspace)}, stream);
-  const auto sums = y.options().dtype(at::kFloat);
   auto [dy, dg, dw, db] = place.allocate([&] {
-    return std::make_tuple(at::empty_like(y), at::empty_like(y), at::empty({y.size(1), y.size(2)}, sums),
-                           at::empty({y.size(1), y.size(2)}, sums));
+    return std::make_tuple(place.fresh(y.sizes(), y.scalar_type()), place.fresh(y.sizes(), y.scalar_type()),
+                           place.fresh({y.size(1), y.size(2)}, at::kFloat), place.fresh({y.size(1), y.size(2)}, at::kFloat));
   });
   const int st = run_msr_affine_backward(place, y, g, weight, bias, dout, dy, dg, static_cast<float*>(dw.data_ptr()),
                                          static_cast<float*>(db.data_ptr()), eps, workspace);

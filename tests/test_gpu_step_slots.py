@@ -237,6 +237,47 @@ def test_serving_run():
     assert not p[1].any() and torch.isnan(p[[2, 3]]).all()
 
 
+def test_calls_right_behind_one_another():
+    """Launches overlap their predecessor's tail: a chain of all the calls, each reading what the one before
+    wrote, gives the same bits unsynchronised, with a synchronisation after every call, and captured."""
+    hq, kv, dk, dv = 4, 4, 128, 128
+    lens = [90, 0, 300, 1]
+    fused, pool, _, _, gamma, theta = case(lens, hq, kv, dk, dv, "bf16", 210, behind=0, n_slots=8)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32).cuda()  # noqa: E731
+    x = fused.cuda()
+    q, k, v = split(x, hq, kv, dk, dv)
+    cu, slots, back, rows = cu_of(lens).cuda(), i32([0, 1, 2, 3]), i32([4, 5, 6, 7]), i32([4, 6, 7])
+    pos = torch.full((4,), 5).cuda()
+    w, b = torch.rand(hq, dv, device="cuda"), torch.rand(hq, dv, device="cuda")
+    ws = torch.empty(rn.retnet_packed_workspace_size((q.shape[0], 4, hq, kv, dk, dv)), dtype=torch.uint8, device="cuda")
+
+    def chain(p, o, sync):
+        for _ in range(4):
+            for call in (lambda: rn.retnet_retention_packed(q, k, v, o, p, cu, slots, pos, gamma, theta, workspace=ws),
+                         lambda: rn.retnet_state_slots_copy(p, slots, back),
+                         lambda: rn.retnet_retention_step_slots(q[:3], k[:3], v[:3], o[:3], p, rows, pos[:3], gamma, theta),
+                         lambda: rn.retnet_msr_affine(o, o, w, b, o),
+                         lambda: rn.retnet_state_slots_copy(p, back, slots)):
+                call()
+                if sync:
+                    torch.cuda.synchronize()
+    results = []
+    for how in ("sync", "eager", "graph"):
+        p, o = pool.cuda(), torch.zeros(q.shape[0], hq, dv, dtype=torch.bfloat16, device="cuda")
+        if how == "graph":
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                chain(p, o, False)
+            graph.replay()
+        else:
+            chain(p, o, how == "sync")
+        torch.cuda.synchronize()
+        results.append((p, o))
+    for p, o in results[1:]:
+        assert torch.equal(p, results[0][0]) and torch.equal(o, results[0][1])
+    assert torch.isfinite(results[0][0]).all() and torch.isfinite(results[0][1]).all()
+
+
 def test_step_equals_packed_of_one_token():
     hq, kv, dk, dv = 4, 2, 64, 64
     fused, pool, slots, pos, gamma, theta = case([1] * 9, hq, kv, dk, dv, "f32", 15, behind=0)
