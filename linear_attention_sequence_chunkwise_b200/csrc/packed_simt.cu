@@ -85,24 +85,26 @@ __global__ void __launch_bounds__(kThreads) simt_rotate_kernel(SimtPackedArgs<T>
   }
 }
 
-// Shared-memory operands of one step: a[r][i] (64 values of the first), b[r][j].
-struct Narrow {  // 64 x 64: rows 4 ty, columns 4 tx
-  Two acc[4][2];
-};
-struct Wide {  // 64 x 128: rows 4 ty, columns 4 tx and 64 + 4 tx
-  Two acc[4][4];
-};
-template <int N, int P>
-__device__ __forceinline__ void fma_step(Two (&acc)[4][N], const float (*a)[kPitch], const float (*b)[P], int ty, int tx) {
+// One step of a tile of 64 rows: a[r][i] (the first operand's 64 values), b[r][j].  A thread has R rows from
+// R ty and 2 N columns: 4 tx .., 64 + 4 tx ...
+template <int R, int N, int P>
+__device__ __forceinline__ void fma_step(Two (&acc)[R][N], const float (*a)[kPitch], const float (*b)[P], int ty, int tx) {
 #pragma unroll
   for (int r = 0; r < kStep; ++r) {
-    const float4 x = *reinterpret_cast<const float4*>(&a[r][ty * 4]);
-    const Two xx[4] = {two(x.x), two(x.y), two(x.z), two(x.w)};
+    Two xx[R];
+#pragma unroll
+    for (int i = 0; i < R; i += 4) {
+      const float4 x = *reinterpret_cast<const float4*>(&a[r][ty * R + i]);
+      xx[i] = two(x.x);
+      xx[i + 1] = two(x.y);
+      xx[i + 2] = two(x.z);
+      xx[i + 3] = two(x.w);
+    }
 #pragma unroll
     for (int j = 0; j < N; j += 2) {
       const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(&b[r][j * 32 + tx * 4]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < R; ++i) {
         acc[i][j] = fma2(xx[i], y.x, acc[i][j]);
         acc[i][j + 1] = fma2(xx[i], y.y, acc[i][j + 1]);
       }
@@ -122,7 +124,7 @@ __global__ void __launch_bounds__(kThreads) simt_state_kernel(SimtPackedArgs<T> 
   const int i0 = (blockIdx.z / tv) * kTile, j0 = (blockIdx.z % tv) * kWide;
   const int tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
   const float lg = hp.log2g[h];
-  Wide o = {};
+  Two acc[4][4] = {};
   float4 kr;
   float vr[8];
   const int kt = tid / 16, kc = tid % 16 * 4, vt = tid / 128, vc = tid % 128;
@@ -148,7 +150,7 @@ __global__ void __launch_bounds__(kThreads) simt_state_kernel(SimtPackedArgs<T> 
     for (int i = 0; i < 8; ++i) vs[vt + 2 * i][vc] = vr[i];
     __syncthreads();
     if (t0 + kStep < d.tokens) fetch(t0 + kStep);
-    fma_step(o.acc, ks, vs, ty, tx);
+    fma_step(acc, ks, vs, ty, tx);
     __syncthreads();
   }
   float* w = a.w + (static_cast<int64_t>(blockIdx.x) * a.kv + h) * a.d_k * a.d_v;
@@ -158,7 +160,7 @@ __global__ void __launch_bounds__(kThreads) simt_state_kernel(SimtPackedArgs<T> 
     if (r >= a.d_k) continue;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float2 x = parts(o.acc[i][j]);
+      const float2 x = parts(acc[i][j]);
       const int c = j0 + (j / 2) * 64 + tx * 4 + (j % 2) * 2;
       if (c < a.d_v) w[static_cast<int64_t>(r) * a.d_v + c] = x.x;
       if (c + 1 < a.d_v) w[static_cast<int64_t>(r) * a.d_v + c + 1] = x.y;
@@ -201,9 +203,12 @@ __global__ void __launch_bounds__(kThreads) simt_scan_kernel(SimtPackedArgs<T> a
   *slot = r;
 }
 
-// grid (units x row tiles, heads, tiles of d_v)
+// grid (units x row tiles, heads, tiles of d_v).  128 threads of 8 x 8 values: with 256 of 4 x 8 the loads
+// from shared memory, three for 16 packed FMAs instead of four for 32, held the warps up for most of the
+// time.
+constexpr int kOutThreads = 128;
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 3) simt_output_kernel(SimtPackedArgs<T> a, HeadParams hp) {
+__global__ void __launch_bounds__(kOutThreads, 3) simt_output_kernel(SimtPackedArgs<T> a, HeadParams hp) {
   __shared__ __align__(16) float as[kStep][kPitch], bs[kStep][kWidePitch];
   __shared__ __align__(16) float ps[kTile][kPitch];  // [key][row]
   pdl_wait();
@@ -212,60 +217,67 @@ __global__ void __launch_bounds__(kThreads, 3) simt_output_kernel(SimtPackedArgs
   const RunDesc d = a.desc[unit];
   const int r0 = blockIdx.x % tiles * kTile;
   if (r0 >= d.tokens) return;
+  constexpr int R = 8;
   const int hq = blockIdx.y, h = hq / a.group, j0 = blockIdx.z * kWide;
   const int tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
   const float lg = hp.log2g[h];
-  // four values (i0 + 4 (tid % 4) ..) of token base + tid / 4, to be transposed into a step
-  const int ht = tid / 4, hc = tid % 4 * 4, bt = tid / 128, bc = tid % 128;
+  // values i0 + hc .. i0 + hc + 3 of tokens base + ht and base + ht + 32, to be transposed into a step
+  const int ht = tid / 4, hc = tid % 4 * 4;
+  struct Heads {
+    float4 x[2];
+  };
   auto head = [&](const float* p, int heads, int which, int base, int i0) {
-    const int t = base + ht;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (t < d.tokens && i0 + hc < a.pitch)
-      x = *reinterpret_cast<const float4*>(p + (static_cast<int64_t>(d.row + t) * heads + which) * a.pitch + i0 + hc);
-    return x;
+    Heads y;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int t = base + ht + 32 * u;
+      y.x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (t < d.tokens && i0 + hc < a.pitch)
+        y.x[u] = *reinterpret_cast<const float4*>(p + (static_cast<int64_t>(d.row + t) * heads + which) * a.pitch + i0 + hc);
+    }
+    return y;
   };
-  auto put = [&](float* to, int pitch, const float4& x) {
-    to[(hc + 0) * pitch + ht] = x.x;
-    to[(hc + 1) * pitch + ht] = x.y;
-    to[(hc + 2) * pitch + ht] = x.z;
-    to[(hc + 3) * pitch + ht] = x.w;
+  auto put = [&](float* to, int pitch, const Heads& y) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int t = ht + 32 * u;
+      to[(hc + 0) * pitch + t] = y.x[u].x;
+      to[(hc + 1) * pitch + t] = y.x[u].y;
+      to[(hc + 2) * pitch + t] = y.x[u].z;
+      to[(hc + 3) * pitch + t] = y.x[u].w;
+    }
   };
-  Wide o = {};
+  const bool in = j0 + tid < a.d_v;  // a thread's column of a wide step
+  Two o[R][4] = {};
   if (!(d.index == 0 && d.pos == 0)) {  // the state before the run, decayed to each row
-    const float* w = a.w + (unit * a.kv + h) * a.d_k * a.d_v + j0 + bc;
-    float4 qr;
-    float wr[8];
+    const float* w = a.w + (unit * a.kv + h) * a.d_k * a.d_v + j0 + tid;
+    Heads qr;
+    float wr[kStep];
     auto fetch = [&](int i0) {
       qr = head(a.qf, a.heads, hq, r0, i0);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = i0 + bt + 2 * i;
-        wr[i] = r < a.d_k && j0 + bc < a.d_v ? w[static_cast<int64_t>(r) * a.d_v] : 0.f;
-      }
+      for (int i = 0; i < kStep; ++i) wr[i] = i0 + i < a.d_k && in ? w[static_cast<int64_t>(i0 + i) * a.d_v] : 0.f;
     };
     fetch(0);
     for (int i0 = 0; i0 < a.d_k; i0 += kStep) {
       put(&as[0][0], kPitch, qr);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) bs[bt + 2 * i][bc] = wr[i];
+      for (int i = 0; i < kStep; ++i) bs[i][tid] = wr[i];
       __syncthreads();
       if (i0 + kStep < a.d_k) fetch(i0 + kStep);
-      fma_step(o.acc, as, bs, ty, tx);
+      fma_step(o, as, bs, ty, tx);
       __syncthreads();
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float xi = decay_pow(lg, r0 + ty * 4 + i + 1);
+    for (int i = 0; i < R; ++i) {
+      const Two xi = two(decay_pow(lg, r0 + ty * R + i + 1));
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 x = parts(o.acc[i][j]);
-        o.acc[i][j] = two(x.x * xi, x.y * xi);
-      }
+      for (int j = 0; j < 4; ++j) o[i][j] = mul2(o[i][j], xi);
     }
   }
   for (int k0 = 0; k0 <= r0; k0 += kTile) {
-    Narrow sc = {};
-    float4 qr = head(a.qf, a.heads, hq, r0, 0), kr = head(a.kf, a.kv, h, k0, 0);
+    Two sc[R][2] = {};
+    Heads qr = head(a.qf, a.heads, hq, r0, 0), kr = head(a.kf, a.kv, h, k0, 0);
     for (int i0 = 0; i0 < a.d_k; i0 += kStep) {
       put(&as[0][0], kPitch, qr);
       put(&bs[0][0], kWidePitch, kr);
@@ -274,45 +286,50 @@ __global__ void __launch_bounds__(kThreads, 3) simt_output_kernel(SimtPackedArgs
         qr = head(a.qf, a.heads, hq, r0, i0 + kStep);
         kr = head(a.kf, a.kv, h, k0, i0 + kStep);
       }
-      fma_step(sc.acc, as, bs, ty, tx);
+      fma_step(sc, as, bs, ty, tx);
       __syncthreads();
     }
-    float vr[8];
+    float vr[kStep];
     auto fetch = [&](int m0) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int t = k0 + m0 + bt + 2 * i;
-        vr[i] = t < d.tokens && j0 + bc < a.d_v
-                    ? load_f(a.v, static_cast<int64_t>(d.row + t) * a.stride_v + static_cast<int64_t>(h) * a.d_v + j0 + bc)
+      for (int i = 0; i < kStep; ++i) {
+        const int t = k0 + m0 + i;
+        vr[i] = t < d.tokens && in
+                    ? load_f(a.v, static_cast<int64_t>(d.row + t) * a.stride_v + static_cast<int64_t>(h) * a.d_v + j0 + tid)
                     : 0.f;
       }
     };
     fetch(0);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 x = parts(sc.acc[i][j / 2]);
-        const int gap = r0 + ty * 4 + i - k0 - tx * 4 - j;
-        ps[tx * 4 + j][ty * 4 + i] = gap >= 0 ? (j % 2 ? x.y : x.x) * decay_pow(lg, gap) : 0.f;
+      for (int i = 0; i < R; i += 4) {
+        float p[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 x = parts(sc[i + e][j / 2]);
+          const int gap = r0 + ty * R + i + e - k0 - tx * 4 - j;
+          p[e] = gap >= 0 ? (j % 2 ? x.y : x.x) * decay_pow(lg, gap) : 0.f;
+        }
+        *reinterpret_cast<float4*>(&ps[tx * 4 + j][ty * R + i]) = make_float4(p[0], p[1], p[2], p[3]);
       }
     for (int m0 = 0; m0 < kTile; m0 += kStep) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) bs[bt + 2 * i][bc] = vr[i];
+      for (int i = 0; i < kStep; ++i) bs[i][tid] = vr[i];
       __syncthreads();
       if (m0 + kStep < kTile) fetch(m0 + kStep);
-      fma_step(o.acc, ps + m0, bs, ty, tx);
+      fma_step(o, ps + m0, bs, ty, tx);
       __syncthreads();
     }
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int t = r0 + ty * 4 + i;
+  for (int i = 0; i < R; ++i) {
+    const int t = r0 + ty * R + i;
     if (t >= d.tokens) continue;
     const float f = a.factor[static_cast<int64_t>(d.row + t) * a.kv + h];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float2 x = parts(o.acc[i][j]);
+      const float2 x = parts(o[i][j]);
       const int c = j0 + (j / 2) * 64 + tx * 4 + (j % 2) * 2;
       const int64_t at = static_cast<int64_t>(d.row + t) * a.stride_o + static_cast<int64_t>(hq) * a.d_v + c;
       if (c < a.d_v) store_f(a.o, at, x.x * f);
@@ -356,7 +373,8 @@ cudaError_t launch_typed(const PackedCall& c, const HeadParams& hp, cudaStream_t
   if (e == cudaSuccess)
     e = launch_dependent(simt_scan_kernel<T>, dim3(nb, kv, static_cast<unsigned>(c.seqs)), block, 0, s, a, hp);
   if (e == cudaSuccess)
-    e = launch_dependent(simt_output_kernel<T>, dim3(u * (run / kTile), static_cast<unsigned>(c.heads), tv), block, 0, s, a, hp);
+    e = launch_dependent(simt_output_kernel<T>, dim3(u * (run / kTile), static_cast<unsigned>(c.heads), tv),
+                         dim3(kOutThreads), 0, s, a, hp);
   return e;
 }
 
