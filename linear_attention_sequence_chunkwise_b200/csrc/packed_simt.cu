@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kThreads) simt_state_kernel(SimtPackedArgs<T> 
   if (d.tokens == 0) return;
   const int h = blockIdx.y, tv = (a.d_v + kWide - 1) / kWide;
   const int i0 = (blockIdx.z / tv) * kTile, j0 = (blockIdx.z % tv) * kWide;
-  const int tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
+  const int tid = threadIdx.x, ty = tid / 64 * 4 + tid % 32 / 8, tx = tid / 32 % 2 * 8 + tid % 8;  // 4 x 8 lanes a warp
   const float lg = hp.log2g[h];
   Two acc[4][4] = {};
   float4 kr;
@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(kOutThreads, 3) simt_output_kernel(SimtPackedA
   if (r0 >= d.tokens) return;
   constexpr int R = 8;
   const int hq = blockIdx.y, h = hq / a.group, j0 = blockIdx.z * kWide;
-  const int tid = threadIdx.x, ty = tid / 16, tx = tid % 16;
+  const int tid = threadIdx.x, ty = tid / 64 * 4 + tid % 32 / 8, tx = tid / 32 % 2 * 8 + tid % 8;  // 4 x 8 lanes a warp
   const float lg = hp.log2g[h];
   // values i0 + hc .. i0 + hc + 3 of tokens base + ht and base + ht + 32, to be transposed into a step
   const int ht = tid / 4, hc = tid % 4 * 4;
