@@ -172,19 +172,45 @@ __global__ void __launch_bounds__(StateCfg<M, NV>::kThreads, 1)
   // products of even / odd steps done; operands of even / odd steps ready; ring slots filled, free
   __shared__ uint64_t bars[10];
   __shared__ uint32_t tmem_at;
-  pdl_wait();
   const int slices = a.d_v / NV;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int k0 = (blockIdx.z / slices) * M, v0 = (blockIdx.z % slices) * NV;
+  unsigned char* smem = raw_smem + ((1024u - (smem_addr(raw_smem) & 1023u)) & 1023u);
+  const uint32_t sm = smem_addr(smem), s2 = sm + 3 * C::kPlane, sv = s2 + 4 * C::kPlane, s_turns = sv + 3 * C::kVBytes;
+  const uint32_t b_done = smem_addr(&bars[0]), b_ready = smem_addr(&bars[2]), b_full = smem_addr(&bars[4]),
+                 b_free = smem_addr(&bars[7]);
+  if (warp == 0) {
+    tmem_alloc(smem_addr(&tmem_at), C::kCols);
+    tmem_relinquish();  // or another CTA of the SM waits for this one's end
+  }
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(b_done + 8 * i, 1);
+      mbar_init(b_ready + 8 * i, C::kData / 32);
+    }
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(b_full + 8 * i, 1);
+      mbar_init(b_free + 8 * i, 1);
+    }
+    fence_mbar_init();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tm = tmem_at;
+  pdl_wait();
+  pdl_go();  // not before: an output CTA that took this one's tensor memory would wait for it for ever
   // The CTA's chunks: units first .. first + count - 1 of head blockIdx.y, or the items blockIdx.x +
   // i gridDim.x of (head, unit).
   int64_t first = 0, count = 0;
   RunDesc d0{};
   if constexpr (SEQ) {
     first = a.cu[blockIdx.x] / kChunk + blockIdx.x;
-    if (first < 0 || first >= a.units) return;  // cu_seqlens out of order: no run has tokens
-    d0 = a.desc[first];
-    if (d0.tokens == 0 || d0.seq != static_cast<int>(blockIdx.x)) return;
+    if (first >= 0 && first < a.units) d0 = a.desc[first];  // (cu_seqlens out of order: no run has tokens)
+    if (d0.tokens == 0 || d0.seq != static_cast<int>(blockIdx.x)) {
+      if (warp == 0) tmem_dealloc(tm, C::kCols);
+      return;
+    }
     count = d0.runs;
   } else {
     const int64_t items = a.units * a.kv;
@@ -212,30 +238,6 @@ __global__ void __launch_bounds__(StateCfg<M, NV>::kThreads, 1)
     }
     return it;
   };
-  unsigned char* smem = raw_smem + ((1024u - (smem_addr(raw_smem) & 1023u)) & 1023u);
-  const uint32_t sm = smem_addr(smem), s2 = sm + 3 * C::kPlane, sv = s2 + 4 * C::kPlane, s_turns = sv + 3 * C::kVBytes;
-  const uint32_t b_done = smem_addr(&bars[0]), b_ready = smem_addr(&bars[2]), b_full = smem_addr(&bars[4]),
-                 b_free = smem_addr(&bars[7]);
-  if (warp == 0) {
-    tmem_alloc(smem_addr(&tmem_at), C::kCols);
-    tmem_relinquish();  // or another CTA of the SM waits for this one's end
-  }
-  if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(b_done + 8 * i, 1);
-      mbar_init(b_ready + 8 * i, C::kData / 32);
-    }
-    for (int i = 0; i < 3; ++i) {
-      mbar_init(b_full + 8 * i, 1);
-      mbar_init(b_free + 8 * i, 1);
-    }
-    fence_mbar_init();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tm = tmem_at;
-  pdl_go();  // not before: an output CTA that took this one's tensor memory would wait for it for ever
   // n: steps of this CTA so far
   auto products_done = [&](int n) { return mbar_wait(b_done + 8 * (n & 1), (n >> 1) & 1, kDrainBudget); };
   auto filled = [&](int n) { return mbar_wait(b_full + 8 * (n % 3), (n / 3) & 1, kDrainBudget); };
