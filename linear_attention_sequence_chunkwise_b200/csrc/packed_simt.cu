@@ -6,10 +6,12 @@
 //   scan    a sequence's runs in order: R_u = the state before run u (written over W_u),
 //           R <- gamma^len R + W; the last R goes to the pool;
 //   output  o_n = f_n [ sum_{m in run, m<=n} gamma^(n-m) (q'_n . k'_m) v_m + gamma^(n-start+1) q'_n R_u ].
-// Bound by the fp32 FMA rate and by shared memory beside it: tiles of 64 rows x 128 columns, 4 x 8
-// values a thread as packed pairs, operands in steps of 16 through shared memory with the next step's
-// loads in flight.  Runs are 64 tokens (one tile: the least arithmetic) up to states of 128 x 128, 256
-// beyond, where the states of shorter runs would be most of the memory traffic and of the workspace.
+// Bound by the fp32 FMA rate and, with few tokens, by the latency of its five launches: tiles of 64 rows x
+// 128 columns as packed pairs, operands in steps of 16 through shared memory with the next step's loads in
+// flight.  Runs are 64 tokens (one tile: the least arithmetic) up to states of 128 x 256, 256 tokens beyond,
+// where the states of shorter runs would be most of the workspace (2999 fp32 tokens, 8 heads, runs of 64
+// against 256: 125 us against 185 at 128 x 128, 226 against 293 at 128 x 256, 452 against 480 at 256 x 256).
+// 2999 tokens, 8 heads on 2, 80 x 120: 71 us, 39 of them the output kernel at about half the FMA rate.
 #include "fp32x2.cuh"
 #include "packed.cuh"
 #include "pdl.cuh"
@@ -23,7 +25,7 @@ constexpr int kStep = 16;     // depth of one shared-memory step
 constexpr int kThreads = 256;
 constexpr int kPitch = kTile + 4, kWidePitch = kWide + 4;
 
-int run_of(int64_t d_k, int64_t d_v) { return d_k * d_v <= 128 * 128 ? 64 : 256; }
+int run_of(int64_t d_k, int64_t d_v) { return d_k * d_v <= 128 * 256 ? 64 : 256; }
 
 template <typename T>
 struct SimtPackedArgs {

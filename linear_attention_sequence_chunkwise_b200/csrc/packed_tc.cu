@@ -151,7 +151,10 @@ __device__ __forceinline__ void track(float& mx, float a, float b) {
 // rotations), the data warps rotate k and cut it into planes in place and, behind a chunk's last step,
 // take the products of the chunk before out of one of two accumulators, one warp issues the products.
 // A data warp that also issued them held the others up for as long as they ran, and one CTA a chunk
-// spent a third of its 7 us on starting (32 us a call of 768 chunk-heads of 128 x 128).
+// spent a third of its 7 us on starting (32 us for 768 chunk-heads of 128 x 128, now 25).
+// Bound by shared memory: at M 128, NV 256 the 12 products of a step read 144 KB, the data warps and the
+// copies move 144 KB more, 2250 cycles of the 3900 that a step takes (the products alone 2100).  The walk
+// of 10040 tokens by a CTA, the longest of 16381 in two documents: 306 us.
 template <int M, int NV>
 struct StateCfg {
   static constexpr int kData = 512, kThreads = kData + 128;  // a warpgroup for the copying and the issuing warp
@@ -550,7 +553,8 @@ __global__ void __launch_bounds__(kScanThreads) tc_scan_kernel(TcPackedArgs a, H
 // copies: the workspace holds it as the tensor cores take it.
 //   When the data warps did all of this in turn, a 64-column slice cost 4800 cycles at d_k 256; with the
 // issuing and copying warps 2300, bound by shared memory: a product of 64 columns reads as much of q as
-// one of 128, which is what the slices are now.
+// one of 128, which is what the slices are now.  Bound by HBM at d_k 256, d_v 512: q, k, v, the states and
+// o of 16381 tokens and 16 heads are 1.34 GB, in 277 us 4.8 TB/s (74 % of the copy rate).
 template <int DK>
 struct OutCfg {
   static constexpr int kData = DK == 256 ? 512 : 256;
@@ -868,6 +872,11 @@ cudaError_t launch_states(const PackedCall& c, const TcPackedArgs& a, const Head
 // more pass over every chunk's fp32 state, written and read (at d_k 256, d_v 512 more bytes than q, k,
 // v and o together); a sequence's walk takes the time of its longest one, so it needs enough CTAs to
 // fill the GPU, or sequences short enough (two chunks on average) that there is nothing to spread.
+// A call by sequence against one by chunk: 16381 tokens in 2, 16 heads of 256 x 512 (128 CTAs) 579 us
+// against 869; 12800 in 64, 8 heads of 128 x 128 (512) 97 against 126; 157 in 6 (48, short) 15.9 against
+// 23.5; 12289 in 9 (72) 90 against 75; 16000 in 4, 16 heads of 128 x 256 (64) 469 against 278.
+// Slices of 256 columns read k from memory and rotate it for twice as many columns as 128 do: 579 us
+// against 673, and 278 against 343.
 int state_columns(int64_t d_v) { return d_v % 256 == 0 ? 256 : d_v % 128 == 0 ? 128 : 64; }
 bool by_sequence(int64_t rows, int64_t seqs, int64_t heads_kv, int64_t d_k, int64_t d_v) {
   return rows <= 2 * kChunk * seqs ||
