@@ -278,6 +278,56 @@ def test_calls_right_behind_one_another():
     assert torch.isfinite(results[0][0]).all() and torch.isfinite(results[0][1]).all()
 
 
+def test_captured_behind_copies_and_joined_streams():
+    """Each call captured right behind a memset, a copy and a join with another stream's work, and read by a
+    copy right behind it: replays give the eager results."""
+    hq, kv, dk, dv = 2, 2, 64, 64
+    lens = [30, 200]
+    fused, pool, _, _, gamma, theta = case(lens, hq, kv, dk, dv, "bf16", 220, behind=0, n_slots=4)
+    source, start = fused.cuda(), pool.cuda()
+    x, p = torch.empty_like(source), torch.empty_like(start)
+    q, k, v = split(x, hq, kv, dk, dv)
+    i32 = lambda t: torch.tensor(t, dtype=torch.int32).cuda()  # noqa: E731
+    cu, slots, other, pos = cu_of(lens).cuda(), i32([0, 3]), i32([1, 2]), torch.tensor([4, 0]).cuda()
+    w = torch.rand(hq, dv, device="cuda")
+    o, kept = torch.empty(230, hq, dv, dtype=torch.bfloat16, device="cuda"), [torch.empty_like(start) for _ in range(3)]
+    out, last = torch.empty_like(o), torch.empty_like(o)
+    ws = torch.empty(rn.retnet_packed_workspace_size((230, 2, hq, kv, dk, dv)), dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+
+    def work():
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            x.copy_(source)
+        p.copy_(start)
+        o.zero_()
+        here.wait_stream(side)
+        rn.retnet_retention_packed(q, k, v, o, p, cu, slots, pos, gamma, theta, workspace=ws)
+        kept[0].copy_(p)
+        rn.retnet_state_slots_copy(p, slots, other)
+        kept[1].copy_(p)
+        o[:2].zero_()
+        rn.retnet_retention_step_slots(q[:2], k[:2], v[:2], o[:2], p, other, pos, gamma, theta)
+        kept[2].copy_(p)
+        out.zero_()
+        rn.retnet_msr_affine(o, q.contiguous(), w, None, out)
+        last.copy_(out)
+    work()
+    torch.cuda.synchronize()
+    want = [t.clone() for t in (*kept, last)]
+    for t in (*kept, last, x, p, o, out):
+        t.zero_()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        work()
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(want, (*kept, last)):
+        assert torch.equal(a, b)
+
+
 def test_step_equals_packed_of_one_token():
     hq, kv, dk, dv = 4, 2, 64, 64
     fused, pool, slots, pos, gamma, theta = case([1] * 9, hq, kv, dk, dv, "f32", 15, behind=0)
