@@ -152,9 +152,10 @@ __device__ __forceinline__ void track(float& mx, float a, float b) {
 // take the products of the chunk before out of one of two accumulators, one warp issues the products.
 // A data warp that also issued them held the others up for as long as they ran, and one CTA a chunk
 // spent a third of its 7 us on starting (32 us for 768 chunk-heads of 128 x 128, now 25).
-// Bound by shared memory: at M 128, NV 256 the 12 products of a step read 144 KB, the data warps and the
-// copies move 144 KB more, 2250 cycles of the 3900 that a step takes (the products alone 2100).  The walk
-// of 10040 tokens by a CTA, the longest of 16381 in two documents: 306 us.
+// Bound by the data warps (converting a step, taking and rounding a state: 48 % of the issue cycles, the
+// rest waits of warps that run in step) with the products close behind: a step of 64 tokens takes 4000 cycles
+// at M 128, NV 256, its products 2100.  The walk of 10040 tokens, the longest of two documents, takes 340 us
+// by itself; 297 with a third of the products, 315 without the small planes, 264 without both.
 template <int M, int NV>
 struct StateCfg {
   static constexpr int kData = 512, kThreads = kData + 128;  // a warpgroup for the copying and the issuing warp
