@@ -580,9 +580,10 @@ __global__ void __launch_bounds__(OutCfg<DK>::kThreads, OutCfg<DK>::kCtas)
   __shared__ uint64_t bars[3 + 2 * C::kRing + 2 * C::kTeams];
   __shared__ uint32_t tmem_at;
   __shared__ float factor[kChunk];
-  // This grid starts when every CTA of the kernel before it has passed its own wait, so the plan is complete;
-  // it is read past the L1 cache.  The states are not: the copying warp waits before it fetches R (and
-  // before the CTA ends, so that no later kernel runs beside the state kernel).
+  // This grid starts when every CTA of the kernel before it has passed its own wait, so the plan, and all that
+  // came before this call, is complete; the plan is read past the L1 cache, q, k and v are read and o, which
+  // the state kernel does not touch, is written at any time.  The states are not complete: the copying warp
+  // waits before it fetches R (and before the CTA ends, so that no later kernel runs beside the state kernel).
   const RunDesc d = plan_entry(a.desc + blockIdx.x);
   if (d.tokens == 0) {
     pdl_wait();

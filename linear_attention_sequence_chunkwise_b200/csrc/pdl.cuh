@@ -1,9 +1,10 @@
 // pdl.cuh -- programmatic dependent launch: a kernel may start while the one before it in the stream
-// drains, and waits (pdl_wait) before it reads or writes any global memory.  Every kernel launched so
-// waits, so that each still runs behind all that came before it; one that says pdl_go lets the next
-// start sooner.  No pointer of such a kernel is __restrict__: a load that is taken for invariant may move
-// above the wait.  Launches overlap so in a stream of calls: one token for 37 rows of 4 x 100 x 130 states
-// 8.2 -> 5.5 us, a fork of four 512 KB slots 5.1 -> 3.7, 157 packed tokens 18.4 -> 16.2.
+// drains, and waits (pdl_wait) before it reads or writes global memory (tc_output_kernel touches some
+// sooner, and says why it may).  Every kernel launched so waits, so that each still runs behind all that
+// came before it; one that says pdl_go lets the next start sooner.  No pointer of such a kernel is
+// __restrict__: a load that is taken for invariant may move above the wait.  Launches overlap so in a
+// stream of calls: one token for 37 rows of 4 x 100 x 130 states 8.2 -> 5.5 us, a fork of four 512 KB slots
+// 5.1 -> 3.7, 157 packed tokens 18.4 -> 16.2.
 #pragma once
 
 #include <cuda_runtime.h>
