@@ -515,8 +515,8 @@ def retnet_retention_packed(q, k, v, o, pool, cu_seqlens, slots, pos, gamma, the
     q (T, heads, d_k), k (T, heads_kv, d_k), v (T, heads_kv, d_v), o (T, heads, d_v) of one dtype, rows
     strided (views of a fused projection); pool (slots, heads_kv, d_k, d_v) float32; cu_seqlens
     (seqs + 1,) int32, slots (seqs,) int32, pos (seqs,) int64 or None on the device; gamma (heads_kv,),
-    theta (d_k/2,) on the host.  Sequence i starts at position pos[i]: 0 from a zero state, else from
-    pool[slots[i]].  Without a workspace (uint8 CUDA tensor) one is allocated for the call."""
+    theta (d_k/2,) on the host.  Sequence i starts at position pos[i] (up to MAX_POSITION): 0 from a zero
+    state, else from pool[slots[i]].  Without a workspace (uint8 CUDA tensor) one is allocated for the call."""
     _check(_native().retention_packed(q, k, v, o, pool, cu_seqlens, slots, pos, _host(gamma), _host(theta), flags, workspace,
                                       _raw(stream)))
 
