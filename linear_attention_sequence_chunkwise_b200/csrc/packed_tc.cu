@@ -20,6 +20,7 @@
 #include "packed.cuh"
 #include "pdl.cuh"
 #include "sm100_ptx.cuh"
+#include "steps_done.h"
 #include "tensor_map.h"
 
 namespace retnet {
@@ -243,7 +244,13 @@ __global__ void __launch_bounds__(StateCfg<M, NV>::kThreads, 1)
     return it;
   };
   // n: steps of this CTA so far
-  auto products_done = [&](int n) { return mbar_wait(b_done + 8 * (n & 1), (n >> 1) & 1, kDrainBudget); };
+  StepsDone steps;
+  auto products_done = [&](int n) {
+    if (!steps.must_wait(n)) return true;
+    if (!mbar_wait(b_done + 8 * (n & 1), (n >> 1) & 1, kDrainBudget)) return false;
+    steps.waited(n);
+    return true;
+  };
   auto filled = [&](int n) { return mbar_wait(b_full + 8 * (n % 3), (n / 3) & 1, kDrainBudget); };
 
   if (tid >= C::kData) {

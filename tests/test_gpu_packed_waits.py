@@ -1,0 +1,62 @@
+"""The waits of the packed tensor-core kernels: results against the fp64 oracle, and no wait gives up."""
+import numpy as np
+import pytest
+import torch
+
+import linear_attention_sequence_chunkwise_b200 as rn
+from gpu_util import TOL_BF16, TOL_F32, require_gpu
+from serving_util import FLAGS, case, cu_of, errors, reference, split
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _gpu(cuda_lib):
+    require_gpu()
+    for f in (rn.retnet_slot_errors, rn.retnet_debug_wait_timeouts, rn.retnet_fp16_range_errors):
+        f(clear=True)
+    yield
+    assert rn.retnet_slot_errors(clear=True) == 0
+    assert rn.retnet_debug_wait_timeouts(clear=True) == 0
+    assert rn.retnet_fp16_range_errors(clear=True) == 0
+
+
+class Call:
+    """One packed bf16 call on the GPU, to be made again and again on the same inputs."""
+
+    def __init__(self, lens, heads, dk, dv, seed, gamma=None, **kw):
+        gamma = np.linspace(0.95, 0.9999, heads) if gamma is None else gamma
+        self.fused, self.pool, self.slots, self.pos, self.gamma, self.theta = case(lens, heads, heads, dk, dv, "bf16", seed,
+                                                                                   gamma=gamma, **kw)
+        self.lens, self.dims = lens, (heads, heads, dk, dv)
+        self.q, self.k, self.v = split(self.fused.cuda(), *self.dims)
+        self.cu, self.pos_d = cu_of(lens).cuda(), torch.tensor(self.pos).cuda()
+        self.slots_d = torch.tensor(self.slots, dtype=torch.int32).cuda()
+        assert rn.retnet_packed_kernel((self.fused.shape[0], len(lens), *self.dims), rn.BF16, FLAGS, self.gamma) == 1
+
+    def run(self):
+        o = torch.full((self.q.shape[0], self.dims[0], self.dims[3]), 0.25, dtype=torch.bfloat16, device="cuda")
+        p = self.pool.cuda()
+        rn.retnet_retention_packed(self.q, self.k, self.v, o, p, self.cu, self.slots_d, self.pos_d, self.gamma, self.theta)
+        return o, p
+
+    def reference(self):
+        return reference(*split(self.fused, *self.dims), self.pool, self.lens, self.slots, self.pos, self.gamma, self.theta,
+                         FLAGS)
+
+
+@pytest.mark.parametrize("lens,heads,dk,dv", [
+    ([128 * 6 + 65, 128 * 5, 128 * 4 + 64, 128 * 7 + 1] * 2, 24, 64, 64),  # walks by sequence, the shortest products
+    ([128 * 9 + 100, 128 * 8], 4, 64, 64),                                  # chunks dealt out
+    ([128 * 5 + 3] * 6, 16, 128, 128),
+    ([128 * 6 + 120] * 2, 8, 256, 256),
+])
+def test_chunks_of_one_and_two_steps_many_times(lens, heads, dk, dv):
+    """The waits of the data warps (tests/test_packed_steps.py) as they run: the same bits every time."""
+    call = Call(lens, heads, dk, dv, 300 + dk + len(lens))
+    ref, after = call.reference()
+    o, p = call.run()
+    assert errors(o, ref) <= TOL_BF16 and errors(p, after) <= TOL_F32
+    for _ in range(100):
+        again = call.run()
+        assert torch.equal(again[0], o) and torch.equal(again[1], p)
