@@ -166,6 +166,7 @@ size_t packed_simt_workspace_bytes(int64_t rows, int64_t seqs, int64_t heads, in
 size_t packed_tc_workspace_bytes(int64_t rows, int64_t seqs, int64_t heads_kv, int64_t d_k, int64_t d_v);
 cudaError_t launch_packed_tc(const PackedCall& c, const HeadParams& hp, cudaStream_t s);
 cudaError_t packed_wait_timeouts(unsigned int* count, bool clear);
+cudaError_t packed_set_wait_budget(long long cycles);
 cudaError_t packed_fp16_overflows(unsigned int* count, bool clear);
 cudaError_t launch_packed_simt(const PackedCall& c, const HeadParams& hp, cudaStream_t s);
 

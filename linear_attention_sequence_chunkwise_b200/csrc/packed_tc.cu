@@ -243,15 +243,17 @@ __global__ void __launch_bounds__(StateCfg<M, NV>::kThreads, 1)
     }
     return it;
   };
-  // n: steps of this CTA so far
+  // n: steps of this CTA so far.  A wait that gives up ends its role: a data warp's lanes decide together (what
+  // follows is a warp's), the data warps together before they exchange a state (its barriers are for all of
+  // them), and the other two wait, with the full budget, for what they have issued.
   StepsDone steps;
   auto products_done = [&](int n) {
     if (!steps.must_wait(n)) return true;
-    if (!mbar_wait(b_done + 8 * (n & 1), (n >> 1) & 1, kDrainBudget)) return false;
+    if (!__all_sync(0xffffffffu, mbar_wait(b_done + 8 * (n & 1), (n >> 1) & 1))) return false;
     steps.waited(n);
     return true;
   };
-  auto filled = [&](int n) { return mbar_wait(b_full + 8 * (n % 3), (n / 3) & 1, kDrainBudget); };
+  auto filled = [&](int n) { return __all_sync(0xffffffffu, mbar_wait(b_full + 8 * (n % 3), (n / 3) & 1)); };
 
   if (tid >= C::kData) {
     registers_less<32>();
@@ -263,7 +265,7 @@ __global__ void __launch_bounds__(StateCfg<M, NV>::kThreads, 1)
         for (int64_t i = 0; alive && i < count; ++i) {
           const int tokens = item(i).tokens;
           for (int st = 0; st * C::kStep < tokens; ++st, ++n) {
-            if (!(alive = mbar_wait(b_ready + 8 * (n & 1), (n >> 1) & 1, kDrainBudget))) break;
+            if (!(alive = mbar_wait(b_ready + 8 * (n & 1), (n >> 1) & 1))) break;
             tc_fence_after();
             const uint64_t dv = sdesc_sw128(sv + n % 3 * C::kVBytes, C::kStep * 128, 1024);
             const uint64_t dk0 = sdesc_sw128(sm + n % 3 * C::kPlane, C::kStep * 128, 1024);
@@ -282,6 +284,7 @@ __global__ void __launch_bounds__(StateCfg<M, NV>::kThreads, 1)
           chunk += tokens > 0;
         }
         for (int i = n > 3 ? n - 3 : 0; i < n; ++i) mbar_wait(b_free + 8 * (i % 3), (i / 3) & 1, kDrainBudget);
+        for (int i = n > 2 ? n - 2 : 0; i < n; ++i) mbar_wait(b_done + 8 * (i & 1), (i >> 1) & 1, kDrainBudget);
       }
     } else if (warp == C::kData / 32 + 1) {  // ---- copies
       if (lane == 0) {
@@ -293,7 +296,7 @@ __global__ void __launch_bounds__(StateCfg<M, NV>::kThreads, 1)
           const Item it = item(i);
           for (int st = 0; st * C::kStep < it.tokens; ++st, ++n) {
             const int slot = n % 3;
-            if (n >= 3 && !(alive = mbar_wait(b_free + 8 * slot, (n / 3 - 1) & 1, kDrainBudget))) break;
+            if (n >= 3 && !(alive = mbar_wait(b_free + 8 * slot, (n / 3 - 1) & 1))) break;
             const uint32_t bar = b_full + 8 * slot;
             mbar_arrive_expect_tx(bar, C::kPlane + C::kVBytes + C::kTurns);
             const int row = it.row + st * C::kStep;
@@ -302,7 +305,8 @@ __global__ void __launch_bounds__(StateCfg<M, NV>::kThreads, 1)
             bulk_load(s_turns + slot * C::kTurns, a.base + (it.unit * a.d_k + k0) * 8 + st * (C::kStep / 16) * M, C::kTurns, bar);
           }
         }
-        for (int i = n > 3 ? n - 3 : 0; i < n; ++i) filled(i);  // no copy in flight at the end
+        // no copy in flight at the end
+        for (int i = n > 3 ? n - 3 : 0; i < n; ++i) mbar_wait(b_full + 8 * (i % 3), (i / 3) & 1, kDrainBudget);
       }
     }
   } else {  // ---- data
@@ -478,7 +482,9 @@ __global__ void __launch_bounds__(StateCfg<M, NV>::kThreads, 1)
       last_head = it.head;
       last_tokens = it.tokens;
     }
-    if (alive && chunk > 0 && products_done(last_step)) {
+    alive = alive && chunk > 0 && products_done(last_step);
+    if constexpr (SEQ) alive = named_bar_all(1, C::kData, alive);
+    if (alive) {
       take(chunk - 1, SEQ ? decay_of(lg, last_tokens) : full,
            SEQ ? exp2f(static_cast<float>(last_tokens - kChunk) * lg) : 1.f, last_unit, last_head);
       if constexpr (SEQ) exchange_pool(true);
@@ -609,7 +615,11 @@ __global__ void __launch_bounds__(OutCfg<DK>::kThreads, OutCfg<DK>::kCtas)
     return i < C::kOwn ? own + i * C::kPiece : sk + (i - C::kOwn) * C::kPiece;
   };
   auto columns = [&](int s) { return a.d_v - s * NV < NV ? a.d_v - s * NV : NV; };  // 64 or 128
-  auto wait = [](uint32_t bar, int phase) { return mbar_wait(bar, phase & 1, kDrainBudget); };
+  // A wait that gives up ends its role: a warp's lanes decide together (what follows is a warp's), and who has
+  // issued products or copies waits, with the full budget, for those.
+  auto wait = [](uint32_t bar, int phase) { return mbar_wait(bar, phase & 1); };
+  auto wait_all = [](uint32_t bar, int phase) { return __all_sync(0xffffffffu, mbar_wait(bar, phase & 1)); };
+  auto drain = [](uint32_t bar, int phase) { mbar_wait(bar, phase & 1, kDrainBudget); };
   if (warp == 0) {
     tmem_alloc(smem_addr(&tmem_at), C::kCols);
     tmem_relinquish();
@@ -656,7 +666,8 @@ __global__ void __launch_bounds__(OutCfg<DK>::kThreads, OutCfg<DK>::kCtas)
       const uint64_t dq = sdesc_sw128(sq, 16, 1024), dk = sdesc_sw128(sk, 16, 1024);
       auto kstep = [](int ks) -> uint64_t { return static_cast<uint64_t>(((ks / 4) * kBlock + (ks % 4) * 32) >> 4); };
       bool ok = wait(b_qk, 0);
-      if (ok) {
+      const bool scores = ok;
+      if (scores) {
         tc_fence_after();
         constexpr uint32_t ID = idesc_f16_f32(kChunk, kChunk, 0, 0);
 #pragma unroll
@@ -694,9 +705,9 @@ __global__ void __launch_bounds__(OutCfg<DK>::kThreads, OutCfg<DK>::kCtas)
         mma_commit(b_done + 8 * team);
       }
       // nothing in flight when the tensor memory is freed
-      wait(b_s, 0);
-      for (int i = n > C::kRing ? n - C::kRing : 0; i < n; ++i) wait(b_free + 8 * (i % C::kRing), i / C::kRing);
-      if (s > 0) wait(b_done + 8 * ((s - 1) % C::kTeams), (s - 1) / C::kTeams);
+      if (scores) drain(b_s, 0);
+      for (int i = n > C::kRing ? n - C::kRing : 0; i < n; ++i) drain(b_free + 8 * (i % C::kRing), i / C::kRing);
+      if (s > 0) drain(b_done + 8 * ((s - 1) % C::kTeams), (s - 1) / C::kTeams);
     }
   } else if (warp == C::kData / 32 + 1) {  // ---- V and R
     const __nv_bfloat16* vp = a.v + static_cast<int64_t>(d.row) * a.stride_v + static_cast<int64_t>(h) * a.d_v;
@@ -707,7 +718,7 @@ __global__ void __launch_bounds__(OutCfg<DK>::kThreads, OutCfg<DK>::kCtas)
       for (int p = 0; p < pieces; ++p, ++n) {
         const int i = n % C::kRing;
         const uint32_t to = buffer(n), bar = b_full + 8 * i;
-        ok = n >= C::kRing ? wait(b_free + 8 * i, n / C::kRing - 1) : i < C::kOwn || wait(b_s, 0);
+        ok = n >= C::kRing ? wait_all(b_free + 8 * i, n / C::kRing - 1) : i < C::kOwn || wait_all(b_s, 0);
         if (!ok) break;
         if (p > 0) {
           if (!waited) pdl_wait();
@@ -737,7 +748,7 @@ __global__ void __launch_bounds__(OutCfg<DK>::kThreads, OutCfg<DK>::kCtas)
       }
     }
     if (!waited) pdl_wait();
-    for (int i = n > C::kRing ? n - C::kRing : 0; i < n; ++i) wait(b_full + 8 * (i % C::kRing), i / C::kRing);
+    for (int i = n > C::kRing ? n - C::kRing : 0; i < n; ++i) drain(b_full + 8 * (i % C::kRing), i / C::kRing);
   } else {  // ---- data
     const float lg = hp.log2g[h];
     constexpr int kBase = DK < 128 ? DK : 128;  // columns of a block of the rotations
@@ -782,7 +793,7 @@ __global__ void __launch_bounds__(OutCfg<DK>::kThreads, OutCfg<DK>::kCtas)
     const int quarter = warp % 4, row = quarter * 32 + lane, team = warp / 8;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
     const float back = exp2f(-static_cast<float>(kChunk) * lg);
-    if (wait(b_s, 0)) {
+    if (wait_all(b_s, 0)) {
       tc_fence_after();
 #pragma unroll
       for (int c = (warp / 4) * 32; c < kChunk; c += C::kData / 4) {
@@ -807,7 +818,7 @@ __global__ void __launch_bounds__(OutCfg<DK>::kThreads, OutCfg<DK>::kCtas)
       __nv_bfloat16* op = a.o + (static_cast<int64_t>(d.row) + row) * a.stride_o + static_cast<int64_t>(hq) * a.d_v + c0;
       const bool in = row < d.tokens, wide = a.o_wide;
       for (int s = team; s < slices; s += C::kTeams) {
-        if (!wait(b_done + 8 * team, s / C::kTeams)) break;
+        if (!wait_all(b_done + 8 * team, s / C::kTeams)) break;
         tc_fence_after();
 #pragma unroll
         for (int c = 0; c < 64; c += 32) {
@@ -961,6 +972,11 @@ cudaError_t launch_packed_tc(const PackedCall& c, const HeadParams& hp, cudaStre
   if (c.d_k == 64) return launch_shape<64>(c, a, hp, s);
   if (c.d_k == 128) return launch_shape<128>(c, a, hp, s);
   return launch_shape<256>(c, a, hp, s);
+}
+
+cudaError_t packed_set_wait_budget(long long cycles) {
+  const long long v = cycles > 0 ? cycles : kDrainBudget;
+  return cudaMemcpyToSymbol(g_wait_budget, &v, sizeof(long long));
 }
 
 cudaError_t packed_wait_timeouts(unsigned int* count, bool clear) {

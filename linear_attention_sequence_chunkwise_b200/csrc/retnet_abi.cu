@@ -407,7 +407,8 @@ retnet_status_t retnet_debug_wait_timeouts(unsigned int* count, int clear) {
 retnet_status_t retnet_debug_set_wait_budget(long long cycles) {
   if (cycles > 0 && cycles < 100) return RETNET_ERR_BAD_PARAM;
   if (cudaDeviceSynchronize() != cudaSuccess) return RETNET_ERR_CUDA;
-  return from_cuda(tc_set_wait_budget(cycles));
+  const retnet_status_t st = from_cuda(tc_set_wait_budget(cycles));
+  return st != RETNET_OK ? st : from_cuda(packed_set_wait_budget(cycles));
 }
 
 retnet_status_t retnet_fp16_range_errors(unsigned int* count, int clear) {

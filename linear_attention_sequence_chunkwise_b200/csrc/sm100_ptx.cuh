@@ -175,6 +175,20 @@ __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
+// The same barrier with a vote: whether `mine` holds for every one of its threads (alike within a warp).
+__device__ __forceinline__ bool named_bar_all(uint32_t id, uint32_t threads, bool mine) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %3, 0;\n\t"
+      "bar.red.and.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(all)
+      : "r"(id), "r"(threads), "r"(mine ? 1u : 0u)
+      : "memory");
+  return all != 0;
+}
+
 // Moves registers between the warps of a CTA: all four warps of a warpgroup, within what the CTA was
 // launched with.
 template <int N>

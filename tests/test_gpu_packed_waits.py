@@ -60,3 +60,29 @@ def test_chunks_of_one_and_two_steps_many_times(lens, heads, dk, dv):
     for _ in range(100):
         again = call.run()
         assert torch.equal(again[0], o) and torch.equal(again[1], p)
+
+
+@pytest.mark.parametrize("lens,heads,dk,dv", [
+    ([700, 130, 1, 0, 400], 24, 64, 64),  # a walk by sequence
+    ([1100, 900], 2, 64, 192),            # chunks dealt out, then the scan
+    ([700, 500] * 4, 8, 128, 256),        # by sequence, 64 state values a thread
+    ([900, 1030], 2, 256, 128),           # dealt out, two blocks of d_k, two teams
+])
+def test_waits_that_give_up_return_and_leave_no_trace(lens, heads, dk, dv):
+    """With a budget of 500 SM cycles (a testing aid) the warps' waits for one another give up: the call
+    returns, counts them, and a later call has the bits of an earlier one."""
+    call = Call(lens, heads, dk, dv, 340 + dk + dv)
+    o, p = call.run()
+    assert rn.retnet_debug_wait_timeouts(clear=True) == 0
+    rn.retnet_debug_set_wait_budget(500)
+    try:
+        call.run()  # (its outputs and slots are undefined)
+        torch.cuda.synchronize()
+        gave_up = rn.retnet_debug_wait_timeouts(clear=True)
+    finally:
+        rn.retnet_debug_set_wait_budget(0)
+    rn.retnet_fp16_range_errors(clear=True)  # (so are the operands of the call that gave up)
+    print(f"waits that gave up: {gave_up}")
+    assert gave_up > 0
+    again = call.run()
+    assert torch.equal(again[0], o) and torch.equal(again[1], p)
