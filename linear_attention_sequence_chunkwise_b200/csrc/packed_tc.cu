@@ -596,7 +596,8 @@ __global__ void __launch_bounds__(OutCfg<DK>::kThreads, OutCfg<DK>::kCtas)
   // This grid starts when every CTA of the kernel before it has passed its own wait, so the plan, and all that
   // came before this call, is complete; the plan is read past the L1 cache, q, k and v are read and o, which
   // the state kernel does not touch, is written at any time.  The states are not complete: the copying warp
-  // waits before it fetches R (and before the CTA ends, so that no later kernel runs beside the state kernel).
+  // waits before it fetches R (and before the CTA ends, so that no later kernel runs beside the state kernel), and
+  // so do the others before they wait for what depends on R: the state kernel may run for longer than their budget.
   const RunDesc d = plan_entry(a.desc + blockIdx.x);
   if (d.tokens == 0) {
     pdl_wait();
@@ -682,6 +683,7 @@ __global__ void __launch_bounds__(OutCfg<DK>::kThreads, OutCfg<DK>::kCtas)
         const bool wide = columns(s) == NV;
         if (!(ok = s < C::kTeams || wait(b_read + 8 * team, s / C::kTeams - 1))) break;
         for (int p = 0; p < pieces; ++p, ++n) {
+          if (n == 1 && p == 1) pdl_wait();
           if (!(ok = wait(b_full + 8 * (n % C::kRing), n / C::kRing))) break;
           tc_fence_after();
           const uint32_t at = buffer(n);
@@ -813,6 +815,7 @@ __global__ void __launch_bounds__(OutCfg<DK>::kThreads, OutCfg<DK>::kCtas)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(b_p);
+      if (has_r) pdl_wait();
       const float f = factor[row];
       const int c0 = (warp / 4) % 2 * 64;  // this warp's columns of a slice
       __nv_bfloat16* op = a.o + (static_cast<int64_t>(d.row) + row) * a.stride_o + static_cast<int64_t>(hq) * a.d_v + c0;

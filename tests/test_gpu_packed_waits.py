@@ -86,3 +86,21 @@ def test_waits_that_give_up_return_and_leave_no_trace(lens, heads, dk, dv):
     assert gave_up > 0
     again = call.run()
     assert torch.equal(again[0], o) and torch.equal(again[1], p)
+
+
+def test_waits_do_not_count_the_states_running_time():
+    """Output CTAs start beside the walk over the states and wait for it, however long it takes: with one
+    prompt of 40000 tokens among empty sequences, walked for some 1e6 SM cycles, and a budget of 2e5 (a step
+    of the walk takes 4e3, an output CTA 3e4) no wait gives up."""
+    lens = [0] * 100 + [40000] + [0] * 99
+    call = Call(lens, 2, 64, 64, 371, slots=[0] * 100 + [1] + [0] * 99, pos=[0] * 100 + [7] + [0] * 99, n_slots=2)
+    o, p = call.run()
+    torch.cuda.synchronize()
+    rn.retnet_debug_set_wait_budget(200000)
+    try:
+        again = call.run()
+        torch.cuda.synchronize()
+    finally:
+        rn.retnet_debug_set_wait_budget(0)
+    assert rn.retnet_debug_wait_timeouts(clear=True) == 0
+    assert torch.equal(again[0], o) and torch.equal(again[1], p)
