@@ -330,18 +330,21 @@ __global__ void __launch_bounds__(StateCfg<M, NV>::kThreads, 1)
     Decay full{0.f, true};
     __half* r16 = nullptr;
     auto emit = [&](int64_t chunk) {  // the state before chunk `chunk`, rounded
-      __half* to = r16 + chunk * state_size;
+      if (holds) {  // (what is in the other lanes of tensor memory is no state: not to be reported)
+        __half* to = r16 + chunk * state_size;
 #pragma unroll
-      for (int e = 0; e < C::kHold; e += 8) {
-        uint32_t w[4];
+        for (int e = 0; e < C::kHold; e += 8) {
+          uint32_t w[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 x = parts(S[e / 2 + j]);
-          track(mx, x.x, x.y);
-          w[j] = pack_f16x2(x.x, x.y);
+          for (int j = 0; j < 4; ++j) {
+            const float2 x = parts(S[e / 2 + j]);
+            track(mx, x.x, x.y);
+            w[j] = pack_f16x2(x.x, x.y);
+          }
+          *reinterpret_cast<uint4*>(to + e * M) = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        if (holds) *reinterpret_cast<uint4*>(to + e * M) = make_uint4(w[0], w[1], w[2], w[3]);
       }
+      if (M != 128) __syncwarp();
     };
     // S <- decay S + up D, D the products of the CTA's chunk-th chunk; or D to W of (unit, head)
     auto take = [&](int chunk, Decay decay, float up, int64_t unit, int head) {

@@ -104,3 +104,20 @@ def test_waits_do_not_count_the_states_running_time():
         rn.retnet_debug_set_wait_budget(0)
     assert rn.retnet_debug_wait_timeouts(clear=True) == 0
     assert torch.equal(again[0], o) and torch.equal(again[1], p)
+
+
+@pytest.mark.parametrize("lens,heads,dv", [([700, 130, 300] * 4, 24, 64), ([900, 400] * 6, 16, 128)])
+def test_range_report_sees_only_the_states(lens, heads, dv):
+    """A walk with d_k 64 uses half of the lanes of its accumulators: what another call left in the other
+    half is not reported as out of fp16's range."""
+    call = Call(lens, heads, 64, dv, 381)
+    call.run()
+    assert rn.retnet_fp16_range_errors(clear=True) == 0
+    leave = Call([128] * 296, 8, 64, 128, 382)
+    for x in (leave.q, leave.k, leave.v):
+        x.fill_(float("nan"))
+    for _ in range(3):
+        leave.run()
+        assert rn.retnet_fp16_range_errors(clear=True) > 0
+        call.run()
+        assert rn.retnet_fp16_range_errors(clear=True) == 0
