@@ -472,10 +472,12 @@ typedef struct {
  * chunks of 128 tokens; everything else, and RETNET_F_PRECISE, on the fp32 CUDA cores.
  * retnet_packed_kernel tells which.
  * Precision.  The pool is updated as in fp32 arithmetic on both (no bf16 input leaves a range).  The
- * tensor-core outputs use fp16 copies of the rotated q and k, q decayed by up to gamma^128, k by up to
- * gamma^127, and of the states before each chunk: 2^-11 of the value, but no finer than 2^-25 (below a
- * magnitude of 2^-14 the relative accuracy falls), and finite below 65520; roundings outside are counted by
- * retnet_fp16_range_errors.  RETNET_F_PRECISE has neither limit.
+ * tensor-core outputs use fp16 copies of the rotated and decayed q and k, brought to fp16's range by a power
+ * of two for every 8 or 16 tokens, so that their size does not matter: 2^-11 of the value down to 2^-16 of
+ * the largest of those tokens.  The states before each chunk are rounded to fp16 as they are: 2^-11 of the
+ * value, but no finer than 2^-25 (below a magnitude of 2^-14 the relative accuracy falls), and finite below
+ * 65520.  Larger states, and q or k that are not finite, are counted by retnet_fp16_range_errors; states that
+ * are small throughout are not.  RETNET_F_PRECISE has neither limit.
  * A token whose q, k or v is not finite may make the outputs of up to 255 earlier tokens of its own
  * sequence not finite; it reaches no other sequence.
  */

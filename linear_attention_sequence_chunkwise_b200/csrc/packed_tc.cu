@@ -11,9 +11,11 @@
 // bf16 already, so the products are those of fp32 arithmetic and no bf16 input leaves a range.  For
 // the scores q' and k' are rounded to fp16 once (2^-11 of the value at most), decayed to the chunk's
 // ends: (gamma^(r+1) q'_r) . (gamma^(127-c) k'_c) = gamma^128 gamma^(r-c) q'_r . k'_c, one constant
-// factor instead of one a pair; gamma^128 >= 2^-12 keeps both in fp16's normal range.  The masked
-// scores stay in tensor memory as two bf16 numbers (2^-17), so that v is read as it is.  Each
-// rounding outside fp16's range is counted (retnet_fp16_range_errors).
+// factor instead of one a pair.  A warp's rows (8 or 16 of them) are first brought to fp16's upper end by
+// a power of two, so that after a decay of up to gamma^128 >= 2^-12 an element 2^-16 of their largest is
+// still normal; as they were, q and k of size 0.01 lost up to 1.6 % and of 1e-4 everything at gamma 0.94.
+// The masked scores stay in tensor memory as two bf16 numbers (2^-17), so that v is read as it is.  Each
+// rounding outside fp16's range is counted (retnet_fp16_range_errors): of states, and what is not finite.
 #include <algorithm>
 
 #include "fp32x2.cuh"
@@ -560,6 +562,15 @@ __global__ void __launch_bounds__(kScanThreads) tc_scan_kernel(TcPackedArgs a, H
   report_fp16_range(mx);
 }
 
+// The exponent of the power of two that brings magnitudes up to `top` (a bf16's 15 bits) below 2^15 and the
+// largest to 2^14 at least: turned by a rotation, sqrt(2) larger at most, they are below fp16's 65504.  0 where
+// one is not finite; at most 100, so that neither power leaves fp32.
+__device__ __forceinline__ int fit_exponent(uint32_t top) {
+  const int e = static_cast<int>(top >> 7);
+  return e == 255 ? 0 : min(14 + 127 - e, 100);
+}
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+
 // ---- output ----------------------------------------------------------------------------------
 // CTA = (chunk, query head).  The data warps fetch q and k by asynchronous copies, rotate and round
 // them in place, turn the scores into bf16 pairs in tensor memory, and store the outputs: a slice of up
@@ -595,7 +606,9 @@ __global__ void __launch_bounds__(OutCfg<DK>::kThreads, OutCfg<DK>::kCtas)
   // q and k ready; scores done; P ready; per buffer: filled, free; per team: products done, read
   __shared__ uint64_t bars[3 + 2 * C::kRing + 2 * C::kTeams];
   __shared__ uint32_t tmem_at;
-  __shared__ float factor[kChunk];
+  __shared__ float factor[kChunk];                       // of the rows of o
+  __shared__ float undo_q[kChunk];                       // 1 / the power of two in q's row
+  __shared__ __align__(16) float undo_k[kChunk];         // gamma^-128 / the power of two in k's row
   // This grid starts when every CTA of the kernel before it has passed its own wait, so the plan, and all that
   // came before this call, is complete; the plan is read past the L1 cache, q, k and v are read and o, which
   // the state kernel does not touch, is written at any time.  The states are not complete: the copying warp
@@ -764,13 +777,22 @@ __global__ void __launch_bounds__(OutCfg<DK>::kThreads, OutCfg<DK>::kCtas)
     Turn step = load_turn_l2(a.offset + 16 * DK + g * 8);
     if (kRows == 32) step = product(step, step);
     float mx = 0.f;
-    // q by gamma^(t+1), k by gamma^(127-t)
-    auto convert = [&](unsigned char* area, float scale, float grow) {
-      Turn t = scaled(first, scale);
-      const Turn by = scaled(step, grow);
+    // q by gamma^(t+1), k by gamma^(127-t), and the warp's rows by the power of two that fits them; undo: what
+    // takes that off, times `by`, by row (read behind the scores, which wait for all of this)
+    auto convert = [&](unsigned char* area, float scale, float grow, float* undo, float by) {
       uint4 raw[kPer];
+      uint32_t top = 0;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) raw[i] = *reinterpret_cast<const uint4*>(area + mine + i * kRows * 128);
+      for (int i = 0; i < kPer; ++i) {
+        raw[i] = *reinterpret_cast<const uint4*>(area + mine + i * kRows * 128);
+        const uint32_t a = __vmaxu2(raw[i].x & 0x7fff7fffu, raw[i].y & 0x7fff7fffu);
+        const uint32_t b = __vmaxu2(raw[i].z & 0x7fff7fffu, raw[i].w & 0x7fff7fffu);
+        top = __vmaxu2(top, __vmaxu2(a, b));
+      }
+      const int fit = fit_exponent(__reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16)));
+      const float off = by * power_of_two(-fit);
+      Turn t = scaled(first, scale * power_of_two(fit));
+      const Turn next = scaled(step, grow);
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
         const Eight y = turned(raw[i], t);
@@ -784,20 +806,21 @@ __global__ void __launch_bounds__(OutCfg<DK>::kThreads, OutCfg<DK>::kCtas)
           w[2 * e + 1] = pack_f16x2(u.y, v.y);
         }
         *reinterpret_cast<uint4*>(area + mine + i * kRows * 128) = make_uint4(w[0], w[1], w[2], w[3]);
-        if (i + 1 < kPer) t = product(t, by);
+        if (g == 0) undo[tr + i * kRows] = off;
+        if (i + 1 < kPer) t = product(t, next);
       }
     };
     cp_async_wait<1>();
-    convert(smem, decay_pow(lg, tr + 1), decay_pow(lg, kRows));
+    convert(smem, decay_pow(lg, tr + 1), decay_pow(lg, kRows), undo_q, 1.f);
     cp_async_wait<0>();
-    convert(smem + C::kQ, decay_pow(lg, kChunk - 1 - tr), exp2f(-static_cast<float>(kRows) * lg));
+    convert(smem + C::kQ, decay_pow(lg, kChunk - 1 - tr), exp2f(-static_cast<float>(kRows) * lg), undo_k,
+            exp2f(-static_cast<float>(kChunk) * lg));
     report_fp16_range(mx);
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(b_qk);
     const int quarter = warp % 4, row = quarter * 32 + lane, team = warp / 8;
     const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-    const float back = exp2f(-static_cast<float>(kChunk) * lg);
     if (wait_all(b_s, 0)) {
       tc_fence_after();
 #pragma unroll
@@ -807,8 +830,9 @@ __global__ void __launch_bounds__(OutCfg<DK>::kThreads, OutCfg<DK>::kCtas)
         const int keep = c < quarter * 32 ? 31 : c > quarter * 32 ? -1 : lane;  // the row's last column here
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const float x0 = 2 * e <= keep ? __uint_as_float(r[e / 8][2 * e % 16]) * back : 0.f;
-          const float x1 = 2 * e + 1 <= keep ? __uint_as_float(r[e / 8][2 * e % 16 + 1]) * back : 0.f;
+          const float2 back = *reinterpret_cast<const float2*>(&undo_k[c + 2 * e]);
+          const float x0 = 2 * e <= keep ? __uint_as_float(r[e / 8][2 * e % 16]) * back.x : 0.f;
+          const float x1 = 2 * e + 1 <= keep ? __uint_as_float(r[e / 8][2 * e % 16 + 1]) * back.y : 0.f;
           p[0][e] = top_halves(x0, x1);
           const __nv_bfloat162 low = __floats2bfloat162_rn(rest(x0), rest(x1));
           p[1][e] = *reinterpret_cast<const uint32_t*>(&low);
@@ -819,7 +843,7 @@ __global__ void __launch_bounds__(OutCfg<DK>::kThreads, OutCfg<DK>::kCtas)
       __syncwarp();
       if (lane == 0) mbar_arrive(b_p);
       if (has_r) pdl_wait();
-      const float f = factor[row];
+      const float f = factor[row] * undo_q[row];
       const int c0 = (warp / 4) % 2 * 64;  // this warp's columns of a slice
       __nv_bfloat16* op = a.o + (static_cast<int64_t>(d.row) + row) * a.stride_o + static_cast<int64_t>(hq) * a.d_v + c0;
       const bool in = row < d.tokens, wide = a.o_wide;
