@@ -473,12 +473,20 @@ _binding = None
 
 
 def _native():
-    """The compiled tensor side (csrc/torch_binding.cpp), built beside the library."""
+    """The compiled tensor side (csrc/torch_binding.cpp), built beside the library for this torch and Python."""
     global _binding
     if _binding is None:
         import torch  # noqa: F401  (its libraries, before the module that needs them)
         load()
-        from . import _torch_binding
+        from . import _build
+        try:
+            from . import _torch_binding
+        except ImportError as e:
+            raise RuntimeError(f"the torch binding is missing or of another torch ({e}): build it with "
+                               "linear_attention_sequence_chunkwise_b200._build.build()") from e
+        if _torch_binding.built_for != _build.binding_key():
+            raise RuntimeError(f"the torch binding was built for {_torch_binding.built_for}, this is {_build.binding_key()}: "
+                               "build it again with linear_attention_sequence_chunkwise_b200._build.build()")
         _binding = _torch_binding
     return _binding
 

@@ -1,7 +1,12 @@
-"""Build libretnet.so (the C-ABI library and its sm_100a kernels) and its torch binding in-tree."""
+"""Build libretnet.so (the C-ABI library and its sm_100a kernels) and its torch binding in-tree.
+
+The library needs nvcc alone; the binding is built where torch and its headers are, for that torch and
+that Python (binding_key), and again where these have changed.
+"""
 import glob
 import os
 import subprocess
+import sys
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -11,6 +16,7 @@ LIB = os.path.join(PKG, "libretnet.so")
 BINDING = os.path.join(PKG, "_torch_binding.so")  # torch tensors in, calls into libretnet.so out
 BINDING_SRC = os.path.join(CSRC, "torch_binding.cpp")
 BUILD_DIR = os.path.join(ROOT, "_build")
+BINDING_KEY = os.path.join(BUILD_DIR, "torch_binding.key")  # what the binding there is was built for
 
 NVCC_FLAGS = ["-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo",
               "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden", "--expt-relaxed-constexpr", "-diag-suppress", "177"]
@@ -33,8 +39,29 @@ def up_to_date() -> bool:
     return _newer(LIB, _deps())
 
 
+def _torch():
+    """The torch package with what a build against it needs, or None."""
+    try:
+        import torch
+    except ImportError:
+        return None
+    header = os.path.join(os.path.dirname(torch.__file__), "include", "torch", "csrc", "utils", "pybind.h")
+    return torch if os.path.exists(header) else None
+
+
+def binding_key() -> str:
+    """The C++ and Python interfaces that a binding built now is for."""
+    import sysconfig
+
+    import torch
+    return f"torch {torch.__version__}, C++11 ABI {int(torch._C._GLIBCXX_USE_CXX11_ABI)}, {sysconfig.get_config_var('SOABI')}"
+
+
 def binding_up_to_date() -> bool:
-    return _newer(BINDING, [BINDING_SRC, *glob.glob(os.path.join(INCLUDE, "*.h"))])
+    if not _newer(BINDING, [BINDING_SRC, *glob.glob(os.path.join(INCLUDE, "*.h"))]) or not os.path.exists(BINDING_KEY):
+        return False
+    with open(BINDING_KEY) as f:
+        return f.read() == binding_key()
 
 
 def _binding_command(out):
@@ -47,6 +74,7 @@ def _binding_command(out):
                 os.path.join(cuda, "include"), sysconfig.get_paths()["include"], INCLUDE]
     return ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-w",
             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-DTORCH_EXTENSION_NAME=_torch_binding",
+            f'-DRETNET_BINDING_KEY="{binding_key()}"',
             *[f"-I{d}" for d in includes], BINDING_SRC, "-o", out, f"-L{os.path.join(root, 'lib')}", "-lc10", "-lc10_cuda",
             "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-ltorch_python", f"-L{PKG}", "-l:libretnet.so", "-Wl,-rpath,$ORIGIN"]
 
@@ -54,14 +82,24 @@ def _binding_command(out):
 def _build_binding():
     tmp = f"{BINDING}.{os.getpid()}.tmp"
     subprocess.run(_binding_command(tmp), check=True)
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    with open(BINDING_KEY, "w") as f:
+        f.write(binding_key())
     os.replace(tmp, BINDING)
 
 
+def _bring_binding_up(force: bool):
+    if _torch() is None:
+        print("torch or its headers are missing: libretnet.so is built, its torch binding is not", file=sys.stderr)
+    elif force or not binding_up_to_date():
+        _build_binding()
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    """Compile every csrc/*.cu for sm_100a and link libretnet.so, then the torch binding; return the library's path."""
+    """Compile every csrc/*.cu for sm_100a and link libretnet.so, then, where torch is, the torch binding; return
+    the library's path."""
     if not force and up_to_date():
-        if not binding_up_to_date():
-            _build_binding()
+        _bring_binding_up(force)
         return LIB
     nvcc = os.environ.get("NVCC", "nvcc")
     os.makedirs(BUILD_DIR, exist_ok=True)
@@ -83,11 +121,9 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     link = [nvcc, "-shared", "-gencode", "arch=compute_100a,code=sm_100a", *objs, "-o", tmp, "-cudart", "static"]
     subprocess.run(link, check=True)
     os.replace(tmp, LIB)
-    if force or not binding_up_to_date():
-        _build_binding()
+    _bring_binding_up(force)
     return LIB
 
 
 if __name__ == "__main__":
-    import sys
     print(build(force=True, verbose=True, ptxas_info="-v" in sys.argv))

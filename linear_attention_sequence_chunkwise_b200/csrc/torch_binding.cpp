@@ -240,6 +240,7 @@ std::tuple<int, Tensor, Tensor, Tensor, Tensor> msr_affine_backward_new(const Te
 }  // namespace
 
 PYBIND11_MODULE(_torch_binding, m) {
+  m.attr("built_for") = RETNET_BINDING_KEY;
   m.def("retention_packed", &retention_packed);
   m.def("retention_step_slots", &retention_step_slots);
   m.def("state_slots_copy", &state_slots_copy);
