@@ -562,13 +562,23 @@ __global__ void __launch_bounds__(kScanThreads) tc_scan_kernel(TcPackedArgs a, H
   report_fp16_range(mx);
 }
 
-// The exponent of the power of two that brings magnitudes up to `top` (a bf16's 15 bits) below 2^15 and the
-// largest to 2^14 at least: turned by a rotation, sqrt(2) larger at most, they are below fp16's 65504.  0 where
-// one is not finite; at most 100, so that neither power leaves fp32.
-__device__ __forceinline__ int fit_exponent(uint32_t top) {
-  const int e = static_cast<int>(top >> 7);
-  return e == 255 ? 0 : min(14 + 127 - e, 100);
+// The largest magnitude (15 bits) of each half of N 16-byte pieces of bf16; with FINITE of those that are finite.
+template <bool FINITE, int N>
+__device__ __forceinline__ uint32_t largest(const uint4 (&raw)[N]) {
+  auto size = [](uint32_t w) {
+    w &= 0x7fff7fffu;
+    return FINITE ? w & __vcmpltu2(w, 0x7f807f80u) : w;
+  };
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    top = __vmaxu2(top, __vmaxu2(__vmaxu2(size(raw[i].x), size(raw[i].y)), __vmaxu2(size(raw[i].z), size(raw[i].w))));
+  return top;
 }
+// The exponent of the power of two that brings magnitudes up to `top` (a finite bf16's 15 bits) below 2^15 and
+// the largest to 2^14 at least: turned by a rotation, sqrt(2) larger at most, they are below fp16's 65504.  At
+// most 100, so that neither power leaves fp32.
+__device__ __forceinline__ int fit_exponent(uint32_t top) { return min(14 + 127 - static_cast<int>(top >> 7), 100); }
 __device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 
 // ---- output ----------------------------------------------------------------------------------
@@ -781,15 +791,12 @@ __global__ void __launch_bounds__(OutCfg<DK>::kThreads, OutCfg<DK>::kCtas)
     // takes that off, times `by`, by row (read behind the scores, which wait for all of this)
     auto convert = [&](unsigned char* area, float scale, float grow, float* undo, float by) {
       uint4 raw[kPer];
-      uint32_t top = 0;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        raw[i] = *reinterpret_cast<const uint4*>(area + mine + i * kRows * 128);
-        const uint32_t a = __vmaxu2(raw[i].x & 0x7fff7fffu, raw[i].y & 0x7fff7fffu);
-        const uint32_t b = __vmaxu2(raw[i].z & 0x7fff7fffu, raw[i].w & 0x7fff7fffu);
-        top = __vmaxu2(top, __vmaxu2(a, b));
-      }
-      const int fit = fit_exponent(__reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16)));
+      for (int i = 0; i < kPer; ++i) raw[i] = *reinterpret_cast<const uint4*>(area + mine + i * kRows * 128);
+      auto of_warp = [](uint32_t top) { return __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16)); };
+      uint32_t top = of_warp(largest<false>(raw));
+      if (top >= 0x7f80u) top = of_warp(largest<true>(raw));  // (what is not finite stays so at any scale)
+      const int fit = fit_exponent(top);
       const float off = by * power_of_two(-fit);
       Turn t = scaled(first, scale * power_of_two(fit));
       const Turn next = scaled(step, grow);

@@ -92,3 +92,22 @@ def test_one_token_of_zeros_and_one_not_finite():
     torch.cuda.synchronize()
     assert rn.retnet_fp16_range_errors(clear=True) > 0
     assert torch.equal(o2[:100], o[:100]) and not torch.isfinite(o2[120]).any()
+
+
+@pytest.mark.parametrize("dk", [64, 128, 256])
+def test_a_token_that_is_not_finite_costs_its_neighbours_nothing(dk):
+    """Tokens that share their power of two with one whose q is infinite, or that come before one whose k is,
+    meet the bar at sizes that need it."""
+    fused, pool, slots, pos, gamma, theta = case([128, 70], 2, 2, dk, 64, "bf16", 440 + dk, gamma=[0.94, 0.945], pos=[0, 0])
+    q, k, v = split(fused, 2, 2, dk, 64)
+    q, k = ((x.double() * 1e-4).bfloat16() for x in (q, k))
+    ref, _ = reference(q, k, v, pool, [128, 70], slots, pos, gamma, theta, FLAGS)
+    q[100], q[101, 0, 3], k[128 + 50] = float("inf"), float("nan"), float("-inf")
+    o = torch.full((q.shape[0], 2, 64), 0.25, dtype=torch.bfloat16, device="cuda")
+    rn.retnet_retention_packed(q.cuda(), k.cuda(), v.cuda(), o, pool.cuda(), cu_of([128, 70]).cuda(),
+                               torch.tensor(slots, dtype=torch.int32).cuda(), torch.tensor(pos).cuda(), gamma, theta)
+    torch.cuda.synchronize()
+    assert rn.retnet_fp16_range_errors(clear=True) > 0
+    good = [i for i in range(128 + 50) if i not in (100, 101)]
+    assert errors(o[good], ref[good]) <= TOL_BF16
+    assert not torch.isfinite(o[100]).any() and not torch.isfinite(o[101, 0]).any() and torch.isfinite(o[101, 1]).all()
