@@ -464,8 +464,9 @@ typedef struct {
  *   dtype: of q, k, v and o.  gamma: host float[heads_kv]; theta: host float[d_k/2].
  *   flags: XPOS, SCALE_SQRT_D, NORM_D; RETNET_F_NORM_R is RETNET_ERR_UNSUPPORTED;
  *   RETNET_F_PRECISE keeps the call on the fp32 CUDA-core kernels.
- *   workspace: device, 16-byte aligned, at least retnet_packed_workspace_size bytes, in use until
- *   the call's work completes; two calls that share one must be ordered on the device.
+ *   workspace: device, 16-byte aligned, at least retnet_packed_workspace_size bytes (or what
+ *   retnet_packed_call_workspace_size says for this call), in use until the call's work completes; two
+ *   calls that share one must be ordered on the device.
  *   o and pool overlap no other argument.
  * Kernels: bf16 with d_k in {64, 128, 256}, d_v a multiple of 64, strides multiples of 8, 16-byte
  * aligned q, k, v, o and gamma^128 >= 2^-12 for every head runs on the tensor cores (tcgen05), in
@@ -493,8 +494,15 @@ RETNET_API retnet_status_t retnet_retention_packed(const void* q, const void* k,
  */
 RETNET_API int retnet_packed_kernel(retnet_packed_t dims, retnet_dtype_t dtype, uint32_t flags, const float* gamma);
 
-/* Workspace bytes of retnet_retention_packed (strides and slots are not read). */
+/* Workspace bytes that do for every retnet_retention_packed of these dimensions (strides and slots are not read). */
 RETNET_API retnet_status_t retnet_packed_workspace_size(retnet_packed_t dims, size_t* bytes);
+
+/*
+ * Those that one call needs, on the kernels that retnet_packed_kernel names for the same arguments (a call
+ * whose q, k, v or o is not 16-byte aligned: with RETNET_F_PRECISE); often half of the above or less.
+ */
+RETNET_API retnet_status_t retnet_packed_call_workspace_size(retnet_packed_t dims, retnet_dtype_t dtype, uint32_t flags,
+                                                  const float* gamma, size_t* bytes);
 
 /*
  * Its single-token form (§2.2): row i is one token, at absolute position pos[i], of the sequence in

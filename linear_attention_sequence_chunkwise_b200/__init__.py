@@ -46,8 +46,8 @@ EXPORTS = ("retnet_retention_parallel", "retnet_retention_chunkwise", "retnet_re
            "retnet_backward_workspace_size", "retnet_backward_kernel", "retnet_backward_launches",
            "retnet_chunkwise_kernel", "retnet_chunkwise_launches", "retnet_debug_wait_timeouts",
            "retnet_fp16_range_errors", "retnet_debug_set_wait_budget",
-           "retnet_retention_packed", "retnet_packed_kernel", "retnet_packed_workspace_size", "retnet_retention_step_slots",
-           "retnet_state_slots_copy", "retnet_slot_errors", "retnet_msr_affine", "retnet_msr_affine_backward",
+           "retnet_retention_packed", "retnet_packed_kernel", "retnet_packed_workspace_size",
+           "retnet_packed_call_workspace_size", "retnet_retention_step_slots", "retnet_state_slots_copy", "retnet_slot_errors", "retnet_msr_affine", "retnet_msr_affine_backward",
            "retnet_msr_affine_workspace_size", "retnet_status_string", "retnet_version")
 MAX_SLOT_PAIRS = 1024  # RETNET_MAX_SLOT_PAIRS
 MAX_POSITION = 2 ** 52  # RETNET_MAX_POSITION
@@ -135,6 +135,7 @@ def load(path: str = None):
                                             _vp, _sz, _vp]
     lib.retnet_packed_kernel.argtypes = [PackedDims, _i32, _u32, _vp]
     lib.retnet_packed_workspace_size.argtypes = [PackedDims, ctypes.POINTER(_sz)]
+    lib.retnet_packed_call_workspace_size.argtypes = [PackedDims, _i32, _u32, _vp, ctypes.POINTER(_sz)]
     lib.retnet_retention_step_slots.argtypes = [_vp, _vp, _vp, _vp, PackedDims, _i32, _vp, _vp, _u32, _vp, _vp, _vp,
                                                 _vp]
     lib.retnet_state_slots_copy.argtypes = [_vp, _i64, _i64, _vp, _vp, _i64, _vp]
@@ -143,8 +144,8 @@ def load(path: str = None):
     lib.retnet_msr_affine_backward.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64,
                                                ctypes.c_float, _i32, _vp, _sz, _vp]
     lib.retnet_msr_affine_workspace_size.argtypes = [_i64, _i64, _i64, ctypes.POINTER(_sz)]
-    for name in ("retnet_retention_packed", "retnet_packed_kernel", "retnet_packed_workspace_size", "retnet_retention_step_slots",
-                 "retnet_state_slots_copy", "retnet_slot_errors", "retnet_msr_affine", "retnet_msr_affine_backward",
+    for name in ("retnet_retention_packed", "retnet_packed_kernel", "retnet_packed_workspace_size",
+                 "retnet_packed_call_workspace_size", "retnet_retention_step_slots", "retnet_state_slots_copy", "retnet_slot_errors", "retnet_msr_affine", "retnet_msr_affine_backward",
                  "retnet_msr_affine_workspace_size"):
         getattr(lib, name).restype = _i32
     lib.retnet_status_string.argtypes = [_i32]
@@ -501,18 +502,31 @@ def _raw(stream):
 
 
 def retnet_packed_workspace_size(dims) -> int:
-    """Bytes of workspace for retnet_retention_packed; dims = (tokens, seqs, heads, heads_kv, d_k, d_v)."""
+    """Bytes of workspace that do for every retnet_retention_packed of dims = (tokens, seqs, heads, heads_kv, d_k, d_v)."""
     out = ctypes.c_size_t(0)
     _check(load().retnet_packed_workspace_size(PackedDims(*(int(x) for x in dims), 1), ctypes.byref(out)))
+    return out.value
+
+
+def _packed_dims(dims, strides):
+    rows, seqs, heads, kv, dk, dv = (int(x) for x in dims)
+    return PackedDims(rows, seqs, heads, kv, dk, dv, 1, *(strides or (heads * dk, kv * dk, kv * dv, heads * dv)))
+
+
+def retnet_packed_call_workspace_size(dims, in_dtype, flags, gamma, strides=None) -> int:
+    """Bytes of workspace that a retnet_retention_packed of these arguments (those of retnet_packed_kernel) needs."""
+    d, out = _packed_dims(dims, strides), ctypes.c_size_t(0)
+    g = _host_f32(gamma, d.heads_kv)
+    _check(load().retnet_packed_call_workspace_size(d, int(in_dtype), int(flags), None if g is None else g.tobytes(),
+                                                    ctypes.byref(out)))
     return out.value
 
 
 def retnet_packed_kernel(dims, in_dtype, flags, gamma, strides=None):
     """1 if retnet_retention_packed runs on the tensor cores for dims = (tokens, seqs, heads, heads_kv, d_k,
     d_v), 0 for the CUDA cores, negative (-status) if it would be rejected; strides of q, k, v, o: dense."""
-    rows, seqs, heads, kv, dk, dv = (int(x) for x in dims)
-    d = PackedDims(rows, seqs, heads, kv, dk, dv, 1, *(strides or (heads * dk, kv * dk, kv * dv, heads * dv)))
-    g = _host_f32(gamma, kv)
+    d = _packed_dims(dims, strides)
+    g = _host_f32(gamma, d.heads_kv)
     return load().retnet_packed_kernel(d, int(in_dtype), int(flags), None if g is None else g.tobytes())
 
 

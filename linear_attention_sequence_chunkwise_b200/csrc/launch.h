@@ -161,6 +161,7 @@ struct PackedCall {
 // The tensor-core kernels take this call: bf16, d_k 64, 128 or 256, d_v a multiple of 64, rows and
 // pointers on 16-byte boundaries, gamma^128 >= 2^-12 for every head, no RETNET_F_PRECISE.
 bool packed_tc_supported(const PackedCall& c, const HeadParams& hp);
+bool packed_tc_shape(int64_t d_k, int64_t d_v);  // its condition on the widths
 // Bytes of workspace of the two kernel families.
 size_t packed_simt_workspace_bytes(int64_t rows, int64_t seqs, int64_t heads, int64_t heads_kv, int64_t d_k, int64_t d_v);
 size_t packed_tc_workspace_bytes(int64_t rows, int64_t seqs, int64_t heads_kv, int64_t d_k, int64_t d_v);

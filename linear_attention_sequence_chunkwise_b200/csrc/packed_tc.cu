@@ -963,9 +963,11 @@ cudaError_t launch_shape(const PackedCall& c, const TcPackedArgs& a, const HeadP
 
 }  // namespace
 
+bool packed_tc_shape(int64_t d_k, int64_t d_v) { return (d_k == 64 || d_k == 128 || d_k == 256) && d_v % 64 == 0; }
+
 bool packed_tc_supported(const PackedCall& c, const HeadParams& hp) {
   if (c.dtype != RETNET_BF16 || (c.flags & RETNET_F_PRECISE)) return false;
-  if ((c.d_k != 64 && c.d_k != 128 && c.d_k != 256) || c.d_v % 64) return false;
+  if (!packed_tc_shape(c.d_k, c.d_v)) return false;
   if ((c.stride_q | c.stride_k | c.stride_v | c.stride_o) % 8) return false;
   auto ok = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
   if (!ok(c.q) || !ok(c.k) || !ok(c.v) || !ok(c.o)) return false;
@@ -977,7 +979,7 @@ bool packed_tc_supported(const PackedCall& c, const HeadParams& hp) {
 size_t packed_tc_workspace_bytes(int64_t rows, int64_t seqs, int64_t heads_kv, int64_t d_k, int64_t d_v) {
   const size_t units = static_cast<size_t>(packed_units(rows, seqs, kChunk));
   const size_t states = units * static_cast<size_t>(heads_kv * d_k * d_v);
-  const bool chunks = d_v < 64 || !by_sequence(rows, seqs, heads_kv, d_k, d_v);
+  const bool chunks = !by_sequence(rows, seqs, heads_kv, d_k, d_v);
   return 256 + a256(sizeof(RunDesc) * units) + a256(sizeof(float) * units * 8 * static_cast<size_t>(d_k)) +
          a256(sizeof(float) * 17 * static_cast<size_t>(d_k)) + (chunks ? a256(sizeof(float) * states) : 0) + sizeof(__half) * states;
 }

@@ -535,9 +535,9 @@ retnet_status_t retnet_msr_epilogue(const void* y, const void* g, void* out, int
 namespace {
 bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-size_t packed_workspace_bytes(const retnet_packed_t& d) {
-  return std::max(packed_simt_workspace_bytes(d.tokens, d.seqs, d.heads, d.heads_kv, d.d_k, d.d_v),
-                  packed_tc_workspace_bytes(d.tokens, d.seqs, d.heads_kv, d.d_k, d.d_v));
+size_t packed_workspace_bytes(const retnet_packed_t& d, bool tensor_cores) {
+  return tensor_cores ? packed_tc_workspace_bytes(d.tokens, d.seqs, d.heads_kv, d.d_k, d.d_v)
+                      : packed_simt_workspace_bytes(d.tokens, d.seqs, d.heads, d.heads_kv, d.d_k, d.d_v);
 }
 
 // What the packed call and its single-token form check alike; seqs: entries of slots and pos.
@@ -583,11 +583,21 @@ int retnet_packed_kernel(retnet_packed_t dims, retnet_dtype_t dtype, uint32_t fl
              : 0;
 }
 
+retnet_status_t retnet_packed_call_workspace_size(retnet_packed_t dims, retnet_dtype_t dtype, uint32_t flags,
+                                                  const float* gamma, size_t* bytes) {
+  if (!bytes) return RETNET_ERR_NULL_PTR;
+  const int kernel = retnet_packed_kernel(dims, dtype, flags, gamma);
+  if (kernel < 0) return static_cast<retnet_status_t>(-kernel);
+  *bytes = packed_workspace_bytes(dims, kernel == 1);
+  return RETNET_OK;
+}
+
 retnet_status_t retnet_packed_workspace_size(retnet_packed_t dims, size_t* bytes) {
   if (!bytes) return RETNET_ERR_NULL_PTR;
   if (dims.tokens < 0 || dims.seqs < 0 || dims.heads <= 0 || dims.heads_kv <= 0 || dims.d_k <= 0 || dims.d_v <= 0)
     return RETNET_ERR_BAD_SHAPE;
-  *bytes = packed_workspace_bytes(dims);
+  *bytes = packed_workspace_bytes(dims, false);
+  if (packed_tc_shape(dims.d_k, dims.d_v)) *bytes = std::max(*bytes, packed_workspace_bytes(dims, true));
   return RETNET_OK;
 }
 
@@ -603,13 +613,13 @@ retnet_status_t retnet_retention_packed(const void* q, const void* k, const void
   PackedCall c = packed_call(q, k, v, o, dims, dtype, flags, cu_seqlens, slots, pos, pool);
   if ((st = check_packed_pointers(c)) != RETNET_OK) return st;
   if (!cu_seqlens || !workspace) return RETNET_ERR_NULL_PTR;
-  if (!aligned_to(cu_seqlens, 4) || !aligned16(workspace) ||
-      workspace_bytes < packed_workspace_bytes(dims))
+  const bool tensor_cores = packed_tc_supported(c, hp);
+  if (!aligned_to(cu_seqlens, 4) || !aligned16(workspace) || workspace_bytes < packed_workspace_bytes(dims, tensor_cores))
     return RETNET_ERR_BAD_PARAM;
   if ((st = check_device()) != RETNET_OK) return st;
   c.ws = workspace;
   c.ws_bytes = workspace_bytes;
-  if (packed_tc_supported(c, hp)) return from_cuda(launch_packed_tc(c, hp, static_cast<cudaStream_t>(stream)));
+  if (tensor_cores) return from_cuda(launch_packed_tc(c, hp, static_cast<cudaStream_t>(stream)));
   return from_cuda(launch_packed_simt(c, hp, static_cast<cudaStream_t>(stream)));
 }
 

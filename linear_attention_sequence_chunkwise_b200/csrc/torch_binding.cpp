@@ -129,8 +129,11 @@ int retention_packed(const Tensor& q, const Tensor& k, const Tensor& v, const Te
   if (workspace.has_value()) {
     ws = *workspace;
   } else {
+    uintptr_t at = 0;
+    for (const Tensor* t : {&q, &k, &v, &o}) at |= reinterpret_cast<uintptr_t>(t->data_ptr());
     size_t need = 0;
-    const retnet_status_t st = retnet_packed_workspace_size(d, &need);
+    const retnet_status_t st =
+        retnet_packed_call_workspace_size(d, dtype_of(q), at % 16 ? flags | RETNET_F_PRECISE : flags, g, &need);
     if (st != RETNET_OK) return st;
     ws = place.bytes(need);
   }
