@@ -531,8 +531,8 @@ RETNET_API retnet_status_t retnet_state_slots_copy(float* pool, int64_t slots, i
                                         void* stream);
 
 /*
- * Count of sequences, rows and pairs that the three calls above left out since the last clear.
- * Synchronises with the device; with clear != 0 the count is reset.  RETNET_OK or RETNET_ERR_CUDA.
+ * Count of sequences, rows and pairs that the three calls above left out on the current device since the
+ * last clear.  Synchronises with the device; with clear != 0 the count is reset.  RETNET_OK or RETNET_ERR_CUDA.
  */
 RETNET_API retnet_status_t retnet_slot_errors(unsigned int* count, int clear);
 

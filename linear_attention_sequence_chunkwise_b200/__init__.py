@@ -485,8 +485,9 @@ def _native():
         except ImportError as e:
             raise RuntimeError(f"the torch binding is missing or of another torch ({e}): build it with "
                                "linear_attention_sequence_chunkwise_b200._build.build()") from e
-        if _torch_binding.built_for != _build.binding_key():
-            raise RuntimeError(f"the torch binding was built for {_torch_binding.built_for}, this is {_build.binding_key()}: "
+        built_for = getattr(_torch_binding, "built_for", "something else")
+        if built_for != _build.binding_key():
+            raise RuntimeError(f"the torch binding was built for {built_for}, this is {_build.binding_key()}: "
                                "build it again with linear_attention_sequence_chunkwise_b200._build.build()")
         _binding = _torch_binding
     return _binding
@@ -558,8 +559,8 @@ def retnet_state_slots_copy(pool, src, dst, stream=None):
 
 
 def retnet_slot_errors(clear=True):
-    """Sequences, rows and pairs that the three calls above left out because their slots, positions or
-    cu_seqlens were wrong, since the last clear (synchronises)."""
+    """Sequences, rows and pairs that the three calls above left out on the current device because their slots,
+    positions or cu_seqlens were wrong, since the last clear (synchronises)."""
     c = ctypes.c_uint(0)
     _check(load().retnet_slot_errors(ctypes.byref(c), 1 if clear else 0))
     return c.value
@@ -608,6 +609,8 @@ def retention_parallel(q, k, v, gamma, theta=None, flags=F_ALL, pos0=0, out_dtyp
 
 
 def msr_affine(y, g, weight=None, bias=None, eps=1e-5, stream=None):
+    """retnet_msr_affine into a new tensor, which autograd does not know (as the calls above):
+    msr_affine_backward is its gradient."""
     status, out = _native().msr_affine_new(y, g, weight, bias, eps, _raw(stream))
     _check(status)
     return out

@@ -154,11 +154,12 @@ __device__ __forceinline__ void track(float& mx, float a, float b) {
 // rotations), the data warps rotate k and cut it into planes in place and, behind a chunk's last step,
 // take the products of the chunk before out of one of two accumulators, one warp issues the products.
 // A data warp that also issued them held the others up for as long as they ran, and one CTA a chunk
-// spent a third of its 7 us on starting (32 us for 768 chunk-heads of 128 x 128, now 25).
-// Bound by the data warps (converting a step, taking and rounding a state: 48 % of the issue cycles, the
+// spent a third of its 7 us on starting (32 us for 768 chunk-heads of 128 x 128, now 26).
+// Bound by the data warps (converting a step, taking and rounding a state: 49 % of the issue cycles, the
 // rest waits of warps that run in step) with the products close behind: a step of 64 tokens takes 4000 cycles
-// at M 128, NV 256, its products 2100.  The walk of 10040 tokens, the longest of two documents, takes 340 us
-// by itself; 297 with a third of the products, 315 without the small planes, 264 without both.
+// at M 128, NV 256, its products 2100.  The walk of 10040 tokens, the longest of two documents, takes 336 to
+// 341 us by itself; 297 with a third of the products, 315 without the small planes, 264 without both.  There
+// 64 state values a thread stand beside the conversion and spill (480 bytes of stores, 316 of loads).
 template <int M, int NV>
 struct StateCfg {
   static constexpr int kData = 512, kThreads = kData + 128;  // a warpgroup for the copying and the issuing warp
@@ -592,7 +593,7 @@ __device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(st
 //   When the data warps did all of this in turn, a 64-column slice cost 4800 cycles at d_k 256; with the
 // issuing and copying warps 2300, bound by shared memory: a product of 64 columns reads as much of q as
 // one of 128, which is what the slices are now.  Bound by HBM at d_k 256, d_v 512: q, k, v, the states and
-// o of 16381 tokens and 16 heads are 1.34 GB, in 277 us 4.8 TB/s (74 % of the copy rate).
+// o of 16381 tokens and 16 heads are 1.34 GB, in 281 us 4.8 TB/s (73 % of the copy rate).
 template <int DK>
 struct OutCfg {
   static constexpr int kData = DK == 256 ? 512 : 256;
@@ -929,11 +930,16 @@ cudaError_t launch_states(const PackedCall& c, const TcPackedArgs& a, const Head
 // more pass over every chunk's fp32 state, written and read (at d_k 256, d_v 512 more bytes than q, k,
 // v and o together); a sequence's walk takes the time of its longest one, so it needs enough CTAs to
 // fill the GPU, or sequences short enough (two chunks on average) that there is nothing to spread.
-// A call by sequence against one by chunk: 16381 tokens in 2, 16 heads of 256 x 512 (128 CTAs) 579 us
-// against 869; 12800 in 64, 8 heads of 128 x 128 (512) 97 against 126; 157 in 6 (48, short) 15.9 against
-// 23.5; 12289 in 9 (72) 90 against 75; 16000 in 4, 16 heads of 128 x 256 (64) 469 against 278.
-// Slices of 256 columns read k from memory and rotate it for twice as many columns as 128 do: 579 us
-// against 673, and 278 against 343.
+// A call by sequence against one by chunk (bursts of 30 calls; sustained, the first takes 674 us): 16381
+// tokens in 2 (the longer 10040), 16 heads of 256 x 512 (128 CTAs) 588 us against 904; 12800 in 64 alike, 8
+// heads of 128 x 128 (512) 105 against 139; 157 in 6 (48, short) 16.5 against 26; 12289 in 9 (72), the longest
+// 4.5 times the shortest, 93 against 84; 16000 in 4 alike, 16 heads of 128 x 256 (64) 260 against 281.
+// The host knows how many sequences there are, not how long each is (and counts empty and padding ones), so
+// one long among many short ones is walked by few CTAs: 12000 tokens and 63 sequences of 1 to 8, 8 heads of
+// 128 x 128, 317 us against 134 by chunk; 12000 and 63 empty ones 282 against 104.
+// Slices of 256 columns read k from memory and rotate it for twice as many columns as 128 do: 588 us
+// against 695 for the documents.  (Where only 128 columns make 96 CTAs they would be the better choice: the
+// 16000 tokens in 4 take 209 us with them, by sequence.)
 int state_columns(int64_t d_v) { return d_v % 256 == 0 ? 256 : d_v % 128 == 0 ? 128 : 64; }
 bool by_sequence(int64_t rows, int64_t seqs, int64_t heads_kv, int64_t d_k, int64_t d_v) {
   return rows <= 2 * kChunk * seqs ||
