@@ -475,7 +475,7 @@ typedef struct {
  * Precision.  The pool is updated as in fp32 arithmetic on both (no bf16 input leaves a range).  The
  * tensor-core outputs use fp16 copies of the rotated and decayed q and k, brought to fp16's range by a power
  * of two for every 8 or 16 tokens, so that their size does not matter: 2^-11 of the value down to 2^-16 of
- * the largest of those tokens.  The states before each chunk are rounded to fp16 as they are: 2^-11 of the
+ * the largest of those tokens (where that is 2^-112 or more).  The states before each chunk are rounded to fp16 as they are: 2^-11 of the
  * value, but no finer than 2^-25 (below a magnitude of 2^-14 the relative accuracy falls), and finite below
  * 65520.  Larger states, and q or k that are not finite, are counted by retnet_fp16_range_errors; states that
  * are small throughout are not.  RETNET_F_PRECISE has neither limit.

@@ -578,8 +578,8 @@ __device__ __forceinline__ uint32_t largest(const uint4 (&raw)[N]) {
 }
 // The exponent of the power of two that brings magnitudes up to `top` (a finite bf16's 15 bits) below 2^15 and
 // the largest to 2^14 at least: turned by a rotation, sqrt(2) larger at most, they are below fp16's 65504.  At
-// most 100, so that neither power leaves fp32.
-__device__ __forceinline__ int fit_exponent(uint32_t top) { return min(14 + 127 - static_cast<int>(top >> 7), 100); }
+// most 126, so that neither power leaves fp32: magnitudes below 2^-112 reach less than 2^14.
+__device__ __forceinline__ int fit_exponent(uint32_t top) { return min(14 + 127 - static_cast<int>(top >> 7), 126); }
 __device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 
 // ---- output ----------------------------------------------------------------------------------

@@ -111,3 +111,13 @@ def test_a_token_that_is_not_finite_costs_its_neighbours_nothing(dk):
     good = [i for i in range(128 + 50) if i not in (100, 101)]
     assert errors(o[good], ref[good]) <= TOL_BF16
     assert not torch.isfinite(o[100]).any() and not torch.isfinite(o[101, 0]).any() and torch.isfinite(o[101, 1]).all()
+
+
+@pytest.mark.parametrize("by_q,by_k,by_v", [(1e-33, 1.0, 1.0), (1.0, 1e-33, 1e33), (1e33, 1.0, 1e-33)])
+def test_the_ends_of_the_range(by_q, by_k, by_v):
+    """Powers of two near the ends of fp32's range (for k, a chunk that starts at position 0: no state is read)."""
+    lens, pos = ([300, 128], None) if by_k == 1.0 and by_v == 1.0 else ([128, 77], [0, 0])
+    o, p, (ref, after) = run(lens, 2, 64, 64, 451, [0.94, 0.99], by_q, by_k, by_v, pos=pos, pool_std=0.5 * by_k * by_v)
+    eo, ep = errors(o, ref), errors(p, after)
+    print(f"q {by_q} k {by_k} v {by_v}: o {eo:.2e} pool {ep:.2e}")
+    assert eo <= TOL_BF16 and ep <= TOL_F32
