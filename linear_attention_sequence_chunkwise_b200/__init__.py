@@ -47,7 +47,8 @@ EXPORTS = ("retnet_retention_parallel", "retnet_retention_chunkwise", "retnet_re
            "retnet_chunkwise_kernel", "retnet_chunkwise_launches", "retnet_debug_wait_timeouts",
            "retnet_fp16_range_errors", "retnet_debug_set_wait_budget",
            "retnet_retention_packed", "retnet_packed_kernel", "retnet_packed_workspace_size",
-           "retnet_packed_call_workspace_size", "retnet_retention_step_slots", "retnet_state_slots_copy", "retnet_slot_errors", "retnet_msr_affine", "retnet_msr_affine_backward",
+           "retnet_packed_call_workspace_size", "retnet_retention_step_slots", "retnet_state_slots_copy",
+           "retnet_slot_errors", "retnet_msr_affine", "retnet_msr_affine_backward",
            "retnet_msr_affine_workspace_size", "retnet_status_string", "retnet_version")
 MAX_SLOT_PAIRS = 1024  # RETNET_MAX_SLOT_PAIRS
 MAX_POSITION = 2 ** 52  # RETNET_MAX_POSITION
@@ -145,7 +146,8 @@ def load(path: str = None):
                                                ctypes.c_float, _i32, _vp, _sz, _vp]
     lib.retnet_msr_affine_workspace_size.argtypes = [_i64, _i64, _i64, ctypes.POINTER(_sz)]
     for name in ("retnet_retention_packed", "retnet_packed_kernel", "retnet_packed_workspace_size",
-                 "retnet_packed_call_workspace_size", "retnet_retention_step_slots", "retnet_state_slots_copy", "retnet_slot_errors", "retnet_msr_affine", "retnet_msr_affine_backward",
+                 "retnet_packed_call_workspace_size", "retnet_retention_step_slots", "retnet_state_slots_copy",
+           "retnet_slot_errors", "retnet_msr_affine", "retnet_msr_affine_backward",
                  "retnet_msr_affine_workspace_size"):
         getattr(lib, name).restype = _i32
     lib.retnet_status_string.argtypes = [_i32]

@@ -932,7 +932,7 @@ cudaError_t launch_states(const PackedCall& c, const TcPackedArgs& a, const Head
 // fill the GPU, or sequences short enough (two chunks on average) that there is nothing to spread.
 // A call by sequence against one by chunk (bursts of 30 calls; sustained, the first takes 674 us): 16381
 // tokens in 2 (the longer 10040), 16 heads of 256 x 512 (128 CTAs) 588 us against 904; 12800 in 64 alike, 8
-// heads of 128 x 128 (512) 105 against 139; 157 in 6 (48, short) 16.5 against 26; 12289 in 9 (72), the longest
+// heads of 128 x 128 (512) 105 against 139; 157 in 6 (48, short) 16.5 against 26; 12289 in 9 (72), the longest up to
 // 4.5 times the shortest, 93 against 84; 16000 in 4 alike, 16 heads of 128 x 256 (64) 260 against 281.
 // The host knows how many sequences there are, not how long each is (and counts empty and padding ones), so
 // one long among many short ones is walked by few CTAs: 12000 tokens and 63 sequences of 1 to 8, 8 heads of
